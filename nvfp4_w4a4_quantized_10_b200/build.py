@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4.so")
 DEBUG_LIB = os.path.join(HERE, "libnvfp4_debug.so")
 SOURCES = ["runtime.cu", "quantize.cu", "gemm.cu", "harmonize.cu", "mxfp4.cu", "host_io.cu", "mma_peak.cu"]
-HEADERS = ["ptx.cuh", "common.h", "block_quant.cuh", os.path.join("..", "..", "include", "nvfp4.h")]
+HEADERS = ["ptx.cuh", "common.h", "block_quant.cuh", "gemm_kernel.cuh", "gemm_host.h", os.path.join("..", "..", "include", "nvfp4.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
