@@ -21,7 +21,9 @@
  * Around them: the offline rewrite of a fused weight's scales to one common
  * global scale (the "pre-harmonized" checkpoint), the running amax of a
  * static calibration, and the MXFP4 format the pages contrast NVFP4 with
- * (32-element blocks, power-of-two scales): its quantizer and GEMM.
+ * (32-element blocks, power-of-two scales): its quantizer and GEMM; the linear
+ * layer over experts (router, grouped quantizer, grouped GEMM); and the block
+ * norm that produces the next layer's activation.
  *
  * Conventions shared by every entry point
  *   - Device pointers are raw CUDA device addresses owned by the caller; the
@@ -97,6 +99,23 @@ typedef enum nvfp4_sf_layout { NVFP4_SF_ROWMAJOR = 0, NVFP4_SF_TCGEN05 = 1 } nvf
 
 /* Largest number of output segments nvfp4_fused_proj accepts. */
 #define NVFP4_MAX_SEGMENTS 16
+
+/* Largest number of groups (experts) of the grouped entry points, and of
+ * experts a token is routed to. */
+#define NVFP4_MAX_GROUPS 512
+#define NVFP4_MAX_TOP_K 32
+
+typedef enum nvfp4_route_norm {
+  NVFP4_ROUTE_SOFTMAX_ALL = 0,  /* softmax over all experts                    */
+  NVFP4_ROUTE_SOFTMAX_TOPK = 1  /* softmax over a token's selected experts      */
+} nvfp4_route_norm;
+typedef enum nvfp4_act { NVFP4_ACT_NONE = 0, NVFP4_ACT_SWIGLU = 1 } nvfp4_act;
+typedef enum nvfp4_gate {
+  NVFP4_GATE_NONE = 0,     /* no gate                     */
+  NVFP4_GATE_LINEAR = 1,   /* b * gate                    */
+  NVFP4_GATE_SIGMOID = 2,  /* b * sigmoid(gate)           */
+  NVFP4_GATE_SILU = 3      /* b * gate * sigmoid(gate)    */
+} nvfp4_gate;
 
 /* Bytes needed for the block scales of a [rows, K] operand in `layout`
  * (0 if rows < 1 or K is not a positive multiple of 16). */
@@ -393,6 +412,159 @@ NVFP4_API nvfp4_status nvfp4_mx_quantize(const void* x, nvfp4_in_dtype dtype, in
 NVFP4_API nvfp4_status nvfp4_mx_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
                            const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, void* out,
                            nvfp4_out_dtype out_dtype, nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The W4A4 linear layer over experts (a mixture of experts' projections) and
+ * the block norm around it.  No counterpart in the pages: their model's
+ * linear layers are dense; these are the same quantizer and GEMM over groups
+ * of rows, each with a weight of its own, and the elementwise step between
+ * two such layers.  A layer runs as
+ *   nvfp4_route             logits -> experts, weights, row order, offsets
+ *   nvfp4_grouped_quantize  tokens gathered into expert order, quantized
+ *   nvfp4_grouped_gemm      up (and gate) projections
+ *   nvfp4_grouped_quantize  SwiGLU of them, quantized (act = SWIGLU)
+ *   nvfp4_grouped_gemm      down projection
+ *   nvfp4_block_norm        weighted sum of each token's expert rows, norms,
+ *                           gate, residual, and the next layer's activation
+ * Groups: rows [group_offsets[g], group_offsets[g+1]) belong to group g.  The
+ * offsets are device memory, int32[n_groups + 1], start at 0, never decrease
+ * and end at most at T (a row capacity the host knows); a group may be empty.
+ * Rows from group_offsets[n_groups] to T are neither read into a result nor
+ * written.  Offsets that break this set the device error word
+ * (NVFP4_ERR_DEVICE from nvfp4_last_device_error), and the call then treats
+ * every group as empty and writes nothing.
+ * Grouped scale layout: the TCGEN05 order with each group starting at a
+ * 128-row scale block of its own, in group order (empty groups take none):
+ * scale j of row r of group g sits where TCGEN05 puts row
+ * 128 * sum_{i<g} ceil(rows_i / 128) + r.  The rows that fill a group's last
+ * block are never read into a result and need no value.
+ * Inference only: no operator of this library has a backward pass.
+ * ------------------------------------------------------------------------ */
+
+/* Router: the top_k experts of each token, their softmax weights, and the
+ * order that sorts the (token, expert) pairs by expert.
+ *   logits  device [M, n_experts] row-major, bf16 or f32.  NaN counts as -inf,
+ *           an expert at -inf is never selected, +inf counts as the largest
+ *           float, -0 as 0.  1 <= n_experts <= NVFP4_MAX_GROUPS.
+ *   top_k   1 .. min(n_experts, NVFP4_MAX_TOP_K)
+ *   expert_ids device int32[M, top_k]: by descending logit, ties to the lowest
+ *           index; -1 where a token has fewer than top_k experts above -inf
+ *   weights device float[M, top_k]: exp(x - max) / sum, the sum over all
+ *           experts (SOFTMAX_ALL) or over the selected (SOFTMAX_TOPK); 0 at -1
+ *   slots   device int32[M, top_k]: row of the pair in the sorted order
+ *           (experts ascending, tokens ascending inside one); -1 at -1
+ *   row_index device int32[M * top_k]: token of each sorted row; -1 past the
+ *           last pair
+ *   group_offsets device int32[n_experts + 1]: first sorted row of each expert
+ *   workspace device, nvfp4_route_workspace_bytes(n_experts) bytes; needs no
+ *           initial value and holds none afterwards.  Calls that can run at
+ *           the same time need one each.
+ * All pointers 16-byte aligned.  The result does not depend on timing.
+ * Errors: INVALID_ARG, UNSUPPORTED (not sm_100, n_experts or top_k beyond the
+ * limits, M * top_k >= 2^31 - 65536), ALIGNMENT, CUDA. */
+NVFP4_API size_t nvfp4_route_workspace_bytes(int n_experts);
+NVFP4_API nvfp4_status nvfp4_route(const void* logits, nvfp4_in_dtype dtype, int64_t M, int n_experts, int top_k,
+                         nvfp4_route_norm norm, int32_t* expert_ids, float* weights, int32_t* slots,
+                         int32_t* row_index, int32_t* group_offsets, void* workspace, size_t workspace_bytes,
+                         nvfp4_stream_t stream);
+
+/* Bytes of the grouped-layout block scales of T rows in n_groups groups,
+ * whatever the offsets: floor((T + 127 min(n_groups, T)) / 128) scale blocks
+ * (0 for T < 1, a bad n_groups, or K not a positive multiple of 16). */
+NVFP4_API size_t nvfp4_grouped_scale_bytes(int64_t T, int n_groups, int64_t K);
+
+/* Activation quantizer of the grouped layer: row t of group g is the NVFP4
+ * encoding (bit for bit nvfp4_quantize's) with global scale global_scales[g] of
+ *   act NONE    x[row_index[t]]         x device [M, K]
+ *   act SWIGLU  silu(a) * b in FP32 for the row [a | b] = x[row_index[t]],
+ *               x device [M, 2K]
+ *   row_index     device int32[T], or NULL for row t itself (then M >= T).  An
+ *                 index outside [0, M) sets the device error word
+ *                 (NVFP4_ERR_DEVICE) and its row is quantized as zeros.
+ *   global_scales device float[n_groups], finite and > 0
+ *   codes         device [T, K/2], 16-byte aligned
+ *   block_scales  device, nvfp4_grouped_scale_bytes(T, n_groups, K) bytes in
+ *                 the grouped layout, 16-byte aligned.  Written for the rows
+ *                 of the groups; padding columns are written as zero, padding
+ *                 rows left as they were.
+ * x finite, 16-byte aligned; K % 32 == 0; other pointers 4-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED (not sm_100, too many groups, T * K / 16
+ * >= 2^31 - 2^20), ALIGNMENT, CUDA. */
+NVFP4_API nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_act act, int64_t M, int64_t K,
+                                    const int32_t* row_index, const int32_t* group_offsets, int n_groups, int64_t T,
+                                    const float* global_scales, uint8_t* codes, uint8_t* block_scales,
+                                    nvfp4_stream_t stream);
+
+/* W4A4 products grouped by expert: for each row t of group g
+ *   out[t, n] = alpha_g * sum_b sA[t,b] sW_g[n,b] sum_{k in b} e2m1(A[t,k]) e2m1(W_g[n,k]),
+ *   alpha_g = 1 / (a_global_scales[g] * w_global_scales[g]) rounded once to FP32,
+ * FP32 accumulation, one rounding to the output type.
+ *   a_codes  device [T, K/2]; a_scales device, grouped layout (see above)
+ *   a_global_scales, w_global_scales  device float[n_groups], finite and > 0
+ *   w_codes  device [n_groups, N, K/2]; w_scales device, n_groups consecutive
+ *            TCGEN05 buffers of nvfp4_scale_bytes(N, K, TCGEN05) bytes
+ *   out      device [T, N] row-major; rows outside the groups left as they were
+ *   workspace, workspace_bytes: device, 16-byte aligned, at least
+ *            nvfp4_grouped_workspace_bytes(T, n_groups) bytes, zero-filled
+ *            before its first use (each launch leaves it zero again); or NULL
+ *            and 0 to use the K-split workspace of the stream, under the rules
+ *            and the capture restriction of nvfp4_gemm.  Two graphs captured
+ *            on one stream that may be replayed at the same time share that
+ *            workspace and would race on it: give each its own.
+ * A mean of fewer than 192 rows a group (T / n_groups) runs weight-streaming
+ * tiles whose K loop is split over the CTAs: progress and the bounded waits as
+ * nvfp4_gemm describes for 16 < M <= 128, nvfp4_set_decode_cooperative
+ * included; the partial sums are added in a fixed order.  More rows run as
+ * 256 x 256 CTA-pair tiles without a workspace.
+ * Codes, scales and out 16-byte aligned, the other pointers 4-byte.
+ * Errors: INVALID_ARG, UNSUPPORTED (not sm_100, too many groups,
+ * n_groups * N >= 2^31 - 65536, a first call during capture with no
+ * workspace), ALIGNMENT, CUDA. */
+NVFP4_API size_t nvfp4_grouped_workspace_bytes(int64_t T, int n_groups);
+NVFP4_API nvfp4_status nvfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_global_scales,
+                                const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scales,
+                                const int32_t* group_offsets, int n_groups, int64_t T, int64_t N, int64_t K, void* out,
+                                nvfp4_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                nvfp4_stream_t stream);
+
+/* Block norm: the step between two linear layers of a block, for rows m < M:
+ *   b = y[m], or with slots  sum_j slot_weights[m, j] * y[slots[m, j]]
+ *   b = b * rsqrt(mean(b^2) + eps) * post_weight     (with post_weight)
+ *   b = b * act(gate[m])                             (with gate)
+ *   v = residual[m] + residual_scale * b             (residual 0 if NULL)
+ *   h = v * rsqrt(mean(v^2) + eps) * pre_weight      (with pre_weight, else v)
+ * in FP32; residual_out = v and out = h are each rounded once, and the codes
+ * encode the unrounded h as nvfp4_quantize encodes its input.
+ *   y        device [y_rows, K] of dtype (bf16 or f32); y_rows = M without slots
+ *   slots, slot_weights  device int32 / float [M, top_k], or both NULL: the
+ *            router's outputs.  A slot of -1 is skipped (its weight is not
+ *            read into the sum); one outside [-1, y_rows) sets the device
+ *            error word (NVFP4_ERR_DEVICE) and is skipped.
+ *   post_weight  device float[post_width] or NULL: the norm runs over runs of
+ *            post_width columns (heads) with the same weights: post_width = K,
+ *            or a power of two from 16 to 512 that divides K
+ *   gate     device [M, K] of dtype, or NULL with NVFP4_GATE_NONE
+ *   residual, residual_out  device [M, K] of dtype, each may be NULL
+ *   pre_weight  device float[K] or NULL
+ *   out      device [M, K] of dtype, or NULL
+ *   codes, block_scales  device [M, K/2] and nvfp4_scale_bytes(M, K, layout)
+ *            bytes, or both NULL; with global_scale and layout as
+ *            nvfp4_quantize (TCGEN05 padding is written as zero).  Without
+ *            codes, global_scale and layout are not looked at.
+ * residual_out and out may each be the same buffer as residual or gate (or y
+ * without slots), element for element; no other overlap is allowed, and not
+ * with each other.  At least one output.  Inputs finite with squares whose row
+ * sum stays below 3e38; eps finite and > 0; residual_scale finite.
+ * K % 32 == 0, K <= 32768.  All pointers 16-byte aligned (slots and their
+ * weights 4-byte).
+ * Errors: INVALID_ARG, UNSUPPORTED (not sm_100, K beyond the limit),
+ * ALIGNMENT, CUDA. */
+NVFP4_API nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, int64_t K, int64_t y_rows,
+                              const int32_t* slots, const float* slot_weights, int top_k, const float* post_weight,
+                              int64_t post_width, const void* gate, nvfp4_gate gate_kind, const void* residual,
+                              float residual_scale, void* residual_out, const float* pre_weight, float eps, void* out,
+                              uint8_t* codes, uint8_t* block_scales, float global_scale, nvfp4_sf_layout layout,
+                              nvfp4_stream_t stream);
 
 /* Element conversions exactly as the quantizer performs them, exposed so the
  * encoders can be checked exhaustively.

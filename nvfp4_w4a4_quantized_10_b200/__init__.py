@@ -39,6 +39,10 @@ IN_BF16, IN_F32 = 0, 1
 OUT_BF16, OUT_F32 = 0, 1
 SF_ROWMAJOR, SF_TCGEN05 = 0, 1
 MAX_SEGMENTS = 16
+MAX_GROUPS, MAX_TOP_K = 512, 32
+ROUTE_SOFTMAX_ALL, ROUTE_SOFTMAX_TOPK = 0, 1
+ACT_NONE, ACT_SWIGLU = 0, 1
+GATE_NONE, GATE_LINEAR, GATE_SIGMOID, GATE_SILU = range(4)
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -69,6 +73,20 @@ _lib.nvfp4_linear.argtypes = [_vp, ctypes.c_int, _i64, _i64, _f32, _vp, _vp, _f3
 _lib.nvfp4_gemm_noalloc.argtypes = [_vp, _vp, _f32, _vp, _vp, _f32, _i64, _i64, _i64, _vp, ctypes.c_int, _vp]
 _lib.nvfp4_fused_proj.argtypes = [_vp, _vp, _f32, _vp, _vp, ctypes.POINTER(_i64), ctypes.POINTER(_f32),
                                   ctypes.c_int, _i64, _i64, _vp, ctypes.c_int, _vp]
+_lib.nvfp4_route_workspace_bytes.restype = ctypes.c_size_t
+_lib.nvfp4_route_workspace_bytes.argtypes = [ctypes.c_int]
+_lib.nvfp4_route.argtypes = [_vp, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, _vp,
+                             _vp, ctypes.c_size_t, _vp]
+_lib.nvfp4_grouped_scale_bytes.restype = ctypes.c_size_t
+_lib.nvfp4_grouped_scale_bytes.argtypes = [_i64, ctypes.c_int, _i64]
+_lib.nvfp4_grouped_quantize.argtypes = [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _vp,
+                                        _vp, _vp, _vp]
+_lib.nvfp4_grouped_workspace_bytes.restype = ctypes.c_size_t
+_lib.nvfp4_grouped_workspace_bytes.argtypes = [_i64, ctypes.c_int]
+_lib.nvfp4_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp,
+                                    ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+_lib.nvfp4_block_norm.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp,
+                                  ctypes.c_int, _vp, _f32, _vp, _vp, _f32, _vp, _vp, _vp, _f32, ctypes.c_int, _vp]
 _lib.nvfp4_convert_e4m3.argtypes = [_vp, _vp, _i64, _vp]
 _lib.nvfp4_convert_e2m1.argtypes = [_vp, _vp, _i64, _vp]
 _lib.nvfp4_last_device_error.argtypes = []
@@ -289,6 +307,140 @@ def alloc_mx_quantized(rows: int, K: int, device, layout: int = SF_TCGEN05):
 def nvfp4_mx_gemm(a_codes, a_scales, w_codes, w_scales, M, N, K, out: torch.Tensor) -> None:
     _check("nvfp4_mx_gemm", _lib.nvfp4_mx_gemm(_ptr(a_codes), _ptr(a_scales), _ptr(w_codes), _ptr(w_scales), M, N,
                                                K, _ptr(out), _out_dtype(out), _stream(out)))
+
+
+def _typed(name: str, t, dtype, shape=None, device=None):
+    """Pointer of an optional device tensor whose type (and shape, and device) the call relies on."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    return _ptr(t)
+
+
+def _room(name: str, t, nbytes: int, device=None):
+    """Pointer of an optional device buffer of at least nbytes bytes."""
+    if t is None:
+        return None
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, not on {device}")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name}: {nbytes} bytes needed, got {t.numel() * t.element_size()}")
+    return _ptr(t)
+
+
+def nvfp4_route_workspace_bytes(n_experts: int) -> int:
+    return int(_lib.nvfp4_route_workspace_bytes(n_experts))
+
+
+def nvfp4_route(logits: torch.Tensor, norm: int, expert_ids: torch.Tensor, weights: torch.Tensor, slots: torch.Tensor,
+                row_index: torch.Tensor, group_offsets: torch.Tensor, workspace: torch.Tensor) -> None:
+    """logits [M, E] -> expert_ids, weights, slots [M, top_k], row_index
+    [M * top_k], group_offsets [E + 1]; workspace: nvfp4_route_workspace_bytes(E) bytes."""
+    M, E = logits.shape
+    k, dev = expert_ids.shape[1], logits.device
+    i32 = torch.int32
+    with torch.cuda.device(dev):
+        _check("nvfp4_route",
+               _lib.nvfp4_route(_ptr(logits), _in_dtype(logits), M, E, k, int(norm),
+                                _typed("expert_ids", expert_ids, i32, (M, k), dev),
+                                _typed("weights", weights, torch.float32, (M, k), dev),
+                                _typed("slots", slots, i32, (M, k), dev),
+                                _typed("row_index", row_index, i32, (M * k,), dev),
+                                _typed("group_offsets", group_offsets, i32, (E + 1,), dev),
+                                _room("workspace", workspace, 0, dev), workspace.numel() * workspace.element_size(),
+                                _stream(logits)))
+
+
+def nvfp4_grouped_scale_bytes(T: int, n_groups: int, K: int) -> int:
+    return int(_lib.nvfp4_grouped_scale_bytes(T, n_groups, K))
+
+
+def alloc_grouped(T: int, n_groups: int, K: int, device):
+    """Empty (codes, scales) buffers for T rows of K in n_groups groups."""
+    codes = torch.empty(T, K // 2, dtype=torch.uint8, device=device)
+    scales = torch.empty(nvfp4_grouped_scale_bytes(T, n_groups, K), dtype=torch.uint8, device=device)
+    return codes, scales
+
+
+def nvfp4_grouped_quantize(x: torch.Tensor, group_offsets: torch.Tensor, global_scales: torch.Tensor,
+                           codes: torch.Tensor, block_scales: torch.Tensor, row_index: torch.Tensor | None = None,
+                           act: int = ACT_NONE) -> None:
+    """Rows of x [M, K] (SwiGLU: [M, 2K]) in group order -> codes [T, K/2] and grouped scales."""
+    T, K = codes.shape[0], 2 * codes.shape[1]
+    E, dev = group_offsets.shape[0] - 1, x.device
+    if x.dim() != 2 or x.shape[1] != (2 * K if act == ACT_SWIGLU else K):
+        raise ValueError(f"x: [M, {2 * K if act == ACT_SWIGLU else K}] expected, got {tuple(x.shape)}")
+    with torch.cuda.device(dev):
+        _check("nvfp4_grouped_quantize",
+               _lib.nvfp4_grouped_quantize(_ptr(x), _in_dtype(x), int(act), x.shape[0], K,
+                                           _typed("row_index", row_index, torch.int32, (T,), dev),
+                                           _typed("group_offsets", group_offsets, torch.int32, (E + 1,), dev), E, T,
+                                           _typed("global_scales", global_scales, torch.float32, (E,), dev),
+                                           _typed("codes", codes, torch.uint8, (T, K // 2), dev),
+                                           _room("block_scales", block_scales, nvfp4_grouped_scale_bytes(T, E, K), dev),
+                                           _stream(x)))
+
+
+def nvfp4_grouped_workspace_bytes(T: int, n_groups: int) -> int:
+    return int(_lib.nvfp4_grouped_workspace_bytes(T, n_groups))
+
+
+def nvfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scales: torch.Tensor,
+                       w_codes: torch.Tensor, w_scales: torch.Tensor, w_global_scales: torch.Tensor,
+                       group_offsets: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
+    """a_codes [T, K/2] with grouped scales times w_codes [E, N, K/2] (scales:
+    E TCGEN05 buffers) -> out [T, N]."""
+    T, K = a_codes.shape[0], 2 * a_codes.shape[1]
+    E, N = w_codes.shape[0], w_codes.shape[1]
+    dev, f32 = out.device, torch.float32
+    if tuple(out.shape) != (T, N):
+        raise ValueError(f"out: shape {(T, N)} expected, got {tuple(out.shape)}")
+    with torch.cuda.device(dev):
+        _check("nvfp4_grouped_gemm",
+               _lib.nvfp4_grouped_gemm(_typed("a_codes", a_codes, torch.uint8, None, dev),
+                                       _room("a_scales", a_scales, nvfp4_grouped_scale_bytes(T, E, K), dev),
+                                       _typed("a_global_scales", a_global_scales, f32, (E,), dev),
+                                       _typed("w_codes", w_codes, torch.uint8, (E, N, K // 2), dev),
+                                       _room("w_scales", w_scales, E * nvfp4_scale_bytes(N, K), dev),
+                                       _typed("w_global_scales", w_global_scales, f32, (E,), dev),
+                                       _typed("group_offsets", group_offsets, torch.int32, (E + 1,), dev), E, T, N, K,
+                                       _ptr(out), _out_dtype(out), _room("workspace", workspace, 0, dev),
+                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                       _stream(out)))
+
+
+def nvfp4_block_norm(y: torch.Tensor, slots: torch.Tensor | None = None, slot_weights: torch.Tensor | None = None,
+                     post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                     gate_kind: int = GATE_NONE, residual: torch.Tensor | None = None, residual_scale: float = 1.0,
+                     residual_out: torch.Tensor | None = None, pre_weight: torch.Tensor | None = None,
+                     eps: float = 1e-6, out: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                     block_scales: torch.Tensor | None = None, global_scale: float = 1.0,
+                     layout: int = SF_TCGEN05) -> None:
+    """y [M, K], or [rows, K] with slots and slot_weights [M, top_k]; post_weight
+    of K columns, or of one head; the other rows [M, K] of y's dtype."""
+    K, dev, f32 = y.shape[1], y.device, torch.float32
+    M, k = (y.shape[0], 0) if slots is None else slots.shape
+    row = (M, K)
+    with torch.cuda.device(dev):
+        _check("nvfp4_block_norm",
+               _lib.nvfp4_block_norm(_ptr(y), _in_dtype(y), M, K, y.shape[0],
+                                     _typed("slots", slots, torch.int32, (M, k), dev),
+                                     _typed("slot_weights", slot_weights, f32, (M, k), dev), k,
+                                     _typed("post_weight", post_weight, f32, None, dev),
+                                     0 if post_weight is None else post_weight.numel(),
+                                     _typed("gate", gate, y.dtype, row, dev), int(gate_kind),
+                                     _typed("residual", residual, y.dtype, row, dev), float(residual_scale),
+                                     _typed("residual_out", residual_out, y.dtype, row, dev),
+                                     _typed("pre_weight", pre_weight, f32, (K,), dev), float(eps),
+                                     _typed("out", out, y.dtype, row, dev),
+                                     _typed("codes", codes, torch.uint8, (M, K // 2), dev),
+                                     _room("block_scales", block_scales, nvfp4_scale_bytes(M, K, layout), dev),
+                                     float(global_scale), int(layout), _stream(y)))
 
 
 def nvfp4_convert_e4m3(x: torch.Tensor, out: torch.Tensor) -> None:

@@ -12,14 +12,17 @@ tensor-map encoder is looked up at run time).
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 SRC_DIR = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4.so")
 DEBUG_LIB = os.path.join(HERE, "libnvfp4_debug.so")
-SOURCES = ["runtime.cu", "quantize.cu", "gemm.cu", "harmonize.cu", "mxfp4.cu", "host_io.cu", "mma_peak.cu"]
-HEADERS = ["ptx.cuh", "common.h", "block_quant.cuh", "gemm_kernel.cuh", "gemm_host.h", os.path.join("..", "..", "include", "nvfp4.h")]
+SOURCES = ["runtime.cu", "quantize.cu", "gemm.cu", "harmonize.cu", "mxfp4.cu", "host_io.cu", "mma_peak.cu", "route.cu",
+           "grouped.cu", "block_norm.cu"]
+HEADERS = ["ptx.cuh", "common.h", "block_quant.cuh", "gemm_kernel.cuh", "gemm_host.h", "groups.cuh",
+           os.path.join("..", "..", "include", "nvfp4.h")]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -37,17 +40,21 @@ def _newer(target, deps):
 def _build_one(lib: str, build_dir: str, defines, force: bool, verbose: bool) -> str:
     os.makedirs(build_dir, exist_ok=True)
     headers = [os.path.normpath(os.path.join(SRC_DIR, h)) for h in HEADERS]
-    objs = []
-    for src in SOURCES:
+
+    def compile_one(src: str) -> str:
         s = os.path.join(SRC_DIR, src)
         o = os.path.join(build_dir, src.replace(".cu", ".o"))
-        objs.append(o)
         if force or _newer(o, [s] + headers):
             cmd = [NVCC] + ARCH + FLAGS + defines + ["-c", s, "-o", o]
             if verbose:
                 cmd += ["-Xptxas", "-v"]
                 print(" ".join(cmd))
             subprocess.run(cmd, check=True)
+        return o
+
+    # sources are independent; the GEMM's many kernel instances dominate
+    with ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as pool:
+        objs = list(pool.map(compile_one, SOURCES))
     if force or _newer(lib, objs):
         cmd = [NVCC] + ARCH + ["-shared", "-o", lib + ".tmp"] + objs + ["-lcudart"]
         subprocess.run(cmd, check=True)

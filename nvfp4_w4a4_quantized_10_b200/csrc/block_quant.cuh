@@ -79,6 +79,11 @@ __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi) {
   return out;
 }
 
+// Offset of scale j of row r in the tensor-core scale layout.
+__device__ __forceinline__ int64_t tc_scale_offset(int64_t r, int64_t j, int64_t kc) {
+  return ((r >> 7) * kc + (j >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (j & 3);
+}
+
 // One thread owns one 16-element block: 32 (bf16) or 64 (f32) contiguous
 // bytes in, 8 bytes of codes and one scale byte out; a warp reads 1 KB
 // (bf16) and writes 256 contiguous bytes of codes.
@@ -190,6 +195,25 @@ __device__ __forceinline__ uint32_t quantize_block(const Block16<kF32>& B, float
     lo = cvt_e2m1x8(y0);
     hi = cvt_e2m1x8(y1);
   }
+  return s;
+}
+
+// The same block from FP32 values with a global scale of its own (groups and
+// fused producers): amax must be the largest magnitude of f.  Bit for bit
+// what quantize_block writes for the same values and scale.
+__device__ __forceinline__ uint32_t quantize_values(const float (&f)[16], float amax, float g, uint32_t& lo,
+                                                    uint32_t& hi) {
+  const float t = __fmul_rn(__fdiv_rn(amax, 6.0f), g);
+  const uint32_t s = cvt_e4m3(t);
+  const float r = recip_entry(g, s);       // 0 for s = 0: codes are signed zeros
+  float y0[8], y1[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    y0[i] = __fmul_rn(f[i], r);
+    y1[i] = __fmul_rn(f[8 + i], r);
+  }
+  lo = cvt_e2m1x8(y0);
+  hi = cvt_e2m1x8(y1);
   return s;
 }
 

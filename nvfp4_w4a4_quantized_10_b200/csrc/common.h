@@ -42,6 +42,8 @@ cudaError_t clear_gemm_scratch(int device);
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline bool finite_positive(float g) {
   uint32_t b;
   std::memcpy(&b, &g, 4);
@@ -55,6 +57,23 @@ inline nvfp4_status cuda_status(cudaError_t e) {
   // a cooperative (co-residency guaranteed) grid that cannot be resident at once
   if (e == cudaErrorCooperativeLaunchTooLarge) return NVFP4_ERR_UNSUPPORTED;
   return NVFP4_ERR_CUDA;
+}
+
+// Launch as a programmatic dependent of the kernel before it on the stream:
+// the kernel may start while that one finishes, and waits
+// (griddepcontrol.wait) before it touches memory.
+template <typename Kernel, typename... A>
+inline cudaError_t launch_pdl(Kernel kern, int grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -95,13 +95,13 @@ cudaError_t get_workspace(const DeviceInfo* d, cudaStream_t st, int bn, Workspac
 // two slots of bn x 128 words per CTA.
 size_t workspace_need(const DeviceInfo* d, int bn);
 
-template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false>
+template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
 cudaError_t set_smem_attr(const DeviceInfo* d) {
-  using Cf = Cfg<BN, SWAP, QX, MX, PAIR>;
+  using Cf = Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>;
   static std::once_flag once[64];
   static cudaError_t attr_err[64];
   std::call_once(once[d->device], [&] {
-    auto kern = nvfp4_gemm_kernel<BN, SWAP, OUT_F32, QX, MX, PAIR>;
+    auto kern = nvfp4_gemm_kernel<BN, SWAP, OUT_F32, QX, MX, PAIR, GROUPED>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::kSmemBytes);
     // all of the SM's unified memory as shared memory: two co-resident CTAs
     // of 114 KB fit only with the full carveout, and a cooperative launch is
@@ -114,14 +114,14 @@ cudaError_t set_smem_attr(const DeviceInfo* d) {
 
 // CTAs of this kernel that can be resident on one SM (occupancy API, with the
 // attributes set above), once per device; 0 if the query fails.
-template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false>
+template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
 int resident_per_sm(const DeviceInfo* d) {
-  using Cf = Cfg<BN, SWAP, QX, MX, PAIR>;
+  using Cf = Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>;
   static std::once_flag once[64];
   static int occ[64];
   std::call_once(once[d->device], [&] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, nvfp4_gemm_kernel<BN, SWAP, OUT_F32, QX, MX, PAIR>,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, nvfp4_gemm_kernel<BN, SWAP, OUT_F32, QX, MX, PAIR, GROUPED>,
                                                       Cf::kThreads, Cf::kSmemBytes) != cudaSuccess) {
       (void)cudaGetLastError();
       n = 0;
@@ -132,11 +132,11 @@ int resident_per_sm(const DeviceInfo* d) {
 }
 
 // grid: number of CTAs (0 = the persistent grid); cluster: CTAs per cluster
-template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false>
-cudaError_t launch(const GemmParams& p, const DeviceInfo* d, cudaStream_t st, int grid = 0, int cluster = 1) {
-  using Cf = Cfg<BN, SWAP, QX, MX, PAIR>;
-  auto kern = nvfp4_gemm_kernel<BN, SWAP, OUT_F32, QX, MX, PAIR>;
-  const cudaError_t ea = set_smem_attr<BN, SWAP, OUT_F32, QX, MX, PAIR>(d);
+template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
+cudaError_t launch(const GemmParamsOf<GROUPED>& p, const DeviceInfo* d, cudaStream_t st, int grid = 0, int cluster = 1) {
+  using Cf = Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>;
+  auto kern = nvfp4_gemm_kernel<BN, SWAP, OUT_F32, QX, MX, PAIR, GROUPED>;
+  const cudaError_t ea = set_smem_attr<BN, SWAP, OUT_F32, QX, MX, PAIR, GROUPED>(d);
   if (ea != cudaSuccess) return ea;
   if (grid == 0) {
     if (SWAP) {
@@ -145,7 +145,7 @@ cudaError_t launch(const GemmParams& p, const DeviceInfo* d, cudaStream_t st, in
       if (decode_cooperative()) {
         // a cooperative grid must be resident at once: at most what the
         // occupancy API admits per SM
-        const int occ = resident_per_sm<BN, SWAP, OUT_F32, QX, MX, PAIR>(d);
+        const int occ = resident_per_sm<BN, SWAP, OUT_F32, QX, MX, PAIR, GROUPED>(d);
         if (occ < per_sm) per_sm = occ < 1 ? 1 : occ;
       }
       const int64_t cap = (int64_t)d->sm_count * per_sm;

@@ -42,7 +42,10 @@
 
 #include "block_quant.cuh"
 #include "common.h"
+#include "groups.cuh"
 #include "ptx.cuh"
+
+#include <type_traits>
 
 namespace nvfp4 {
 
@@ -92,6 +95,18 @@ struct alignas(64) GemmParams {
   uint64_t x_bytes;                  // in-kernel activation X
 };
 
+// Groups of rows, each with a weight of its own (nvfp4_grouped_gemm): the
+// activation rows of group g are [off[g], off[g + 1]), its weight rows
+// [g N, (g + 1) N) of one [E N, K / 2] operand.
+struct GroupedGemmParams : GemmParams {
+  CUtensorMap tmap_q_box[4];   // swapped tiles: activation codes in boxes of 16, 32, 64 and 128 rows
+  const int32_t* offsets;      // device [E + 1]
+  const float* ga;             // device [E], activation and weight global scales
+  const float* gw;
+  int E;
+  int w_blocks;                // 128-row scale blocks of one group's weight
+};
+
 // QX: 0 = the Q operand (activations) arrives quantized, as codes and scales
 // in global memory; 1 / 2 = swapped tiles whose activation X (bf16 / f32) the
 // kernel quantizes itself into shared memory, all of the CTA's K-steps at
@@ -103,7 +118,12 @@ struct alignas(64) GemmParams {
 // rows (plus all 256 rows' scales); the even CTA issues the M = 256 MMAs and
 // scale copies for both (tcgen05 cta_group::2); each CTA drains its own 128
 // accumulator rows.
-template <int BN, bool SWAP, int QX = 0, bool MX = false, bool PAIR = false>
+// GROUPED: the rows are split into groups (experts), each multiplied by a
+// weight of its own; group offsets are read on the device.  Swapped tiles
+// then have up to BN = 128 activation rows of one group, and load and
+// multiply only as many (rounded up to a box of 16, 32, 64 or 128 rows, and
+// to 16 columns of the MMA); CTA-pair tiles never cross a group.
+template <int BN, bool SWAP, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
 struct Cfg {
   static constexpr bool kQx = QX != 0;
   // K per pipeline step: kKB blocks of 64 (one MMA each), 256 deep, as
@@ -178,7 +198,8 @@ struct Cfg {
   static constexpr int kOffSeg = kOffBar + kNumBars * 8;             // segment table: ends, alphas
   static constexpr int kOffMisc = kOffSeg + 2 * 4 * NVFP4_MAX_SEGMENTS;
   static constexpr int kOffRtab = kOffMisc + 16;                     // in-kernel activation: g / e4m3(s)
-  static constexpr int kSmemBytes = kOffRtab + (kQx ? 1024 : 0) + 1024;   // + alignment slack
+  static constexpr int kOffTab = kOffRtab + (kQx ? 1024 : 0);        // grouped: table of groups
+  static constexpr int kSmemBytes = kOffTab + (GROUPED ? (int)sizeof(GroupTable) : 0) + 1024;   // + alignment slack
   // TMEM columns.  Normal 128x256 tiles: the copy warps run ahead of the
   // MMAs, so the scales of successive steps use a ring of regions at the top
   // of TMEM ([320,512) for four 48-column regions); the two accumulator
@@ -207,6 +228,7 @@ struct Cfg {
   static_assert(BN % 16 == 0 && BN <= 256, "MMA N");
   static_assert(!kQx || (SWAP && BN <= 32), "in-kernel activation: swapped tiles, M <= 32");
   static_assert(!(kQx && MX), "in-kernel activation: NVFP4 only");
+  static_assert(!GROUPED || (!kQx && (PAIR || (SWAP && BN == 128))), "grouped: CTA pairs or 128-row swapped tiles");
   static_assert(!PAIR || (!SWAP && BN == 256 && !kQx), "CTA pairs: normal 256 x 256 tiles");
   static constexpr int kMmaM = PAIR ? 2 * kBM : kBM;                 // MMA M (over the pair)
   static constexpr int kGroupTiles = PAIR ? kGroupP / 2 : kGroupP;   // raster group, in tiles of P
@@ -283,6 +305,89 @@ __device__ __forceinline__ bool work_next(const GemmParams& p, WorkIter& w, int&
   return true;
 }
 
+// Work of one CTA of a grouped GEMM, from the table of groups in shared
+// memory.  Swapped: tiles (group, 128 weight rows, 128 activation rows of
+// the group), the last index fastest so that neighbours share the weight,
+// cut into k-steps and shared out over the first min(grid, units) CTAs.
+// CTA pairs: tiles (group, 256 activation rows, 256 weight rows) t = pair,
+// pair + pairs, ..., rastered inside a group as the plain GEMM does.
+struct GroupWork {
+  int64_t u, u_end, U, G;
+  int64_t tile;
+  int kt;
+  bool swap;
+  int g, row0, rows, blk;   // current tile: group, first activation row, rows from there to the group's end, scale block
+  const GroupTable* tab;
+};
+
+__device__ __forceinline__ GroupWork group_work_begin(const GroupedGemmParams& p, bool swap, const GroupTable* tab) {
+  GroupWork w;
+  w.kt = p.kt;
+  w.swap = swap;
+  w.tab = tab;
+  w.tile = 0;
+  w.g = w.row0 = w.rows = w.blk = 0;
+  if (swap) {
+    w.U = (int64_t)tab->blk[p.E] * p.tiles_p * p.kt;
+    w.G = w.U < (int64_t)gridDim.x ? w.U : (int64_t)gridDim.x;
+    const bool has = (int64_t)blockIdx.x < w.G;
+    w.u = has ? unit_begin(blockIdx.x, w.U, w.G) : 0;
+    w.u_end = has ? unit_begin(blockIdx.x + 1, w.U, w.G) : 0;
+  } else {
+    w.U = w.G = 0;
+    w.u = blockIdx.x / 2;
+    w.u_end = (int64_t)tab->blk2[p.E] * p.tiles_q;
+  }
+  return w;
+}
+
+__device__ __forceinline__ bool work_next(const GroupedGemmParams& p, GroupWork& w, int& tp, int& tq, int& kb, int& ke) {
+  if (w.u >= w.u_end) return false;
+  const GroupTable& t = *w.tab;
+  if (w.swap) {
+    w.tile = w.u / w.kt;
+    const int tile = (int)w.tile;
+    const int g = find_group(t.blk, p.E, tile / p.tiles_p);
+    const int local = tile - t.blk[g] * p.tiles_p;
+    const int cnt = t.blk[g + 1] - t.blk[g];
+    tp = local / cnt;
+    tq = local - tp * cnt;
+    kb = (int)(w.u - w.tile * w.kt);
+    const int64_t rest = w.u_end - w.u;
+    ke = (int)(kb + rest < w.kt ? kb + rest : w.kt);
+    w.u += ke - kb;
+    w.g = g;
+    w.row0 = t.off[g] + tq * 128;
+    w.blk = t.blk[g] + tq;
+    w.rows = min(t.off[g + 1] - w.row0, 128);
+  } else {
+    const int tile = (int)w.u;
+    const int g = find_group(t.blk2, p.E, tile / p.tiles_q);
+    const int local = tile - t.blk2[g] * p.tiles_q;
+    const int cnt = t.blk2[g + 1] - t.blk2[g];
+    const int per = p.group_p * p.tiles_q;
+    const int first = local / per * p.group_p;
+    const int gsize = min(cnt - first, p.group_p);
+    const int l2 = local - first * p.tiles_q;
+    tp = first + l2 % gsize;
+    tq = l2 / gsize;
+    kb = 0;
+    ke = w.kt;
+    w.u += gridDim.x / 2;
+    w.g = g;
+    w.row0 = t.off[g] + tp * 256;
+    w.blk = t.blk[g] + tp * 2;
+    w.rows = t.off[g + 1] - w.row0;
+  }
+  return true;
+}
+
+// One tile's operands: first code rows and first 128-row scale blocks of P
+// and Q, and (grouped, swapped) activation rows.
+struct TileSrc {
+  int p0, q0, pb, qb, rows;
+};
+
 // Segment of output column n, from the table the CTA copied to shared memory.
 __device__ __forceinline__ int seg_index_smem(const int* ends, int n_seg, int64_t n) {
   int i = 0;
@@ -320,10 +425,14 @@ __device__ __forceinline__ uint64_t ld_word(const uint64_t* p) {
 // stored with the 128B swizzle the output tensor map uses.
 __device__ __forceinline__ uint32_t swz128(uint32_t r, uint32_t c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
-template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false>
-__global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN, SWAP, QX, MX, PAIR>::kMinBlocks)
-    nvfp4_gemm_kernel(const __grid_constant__ GemmParams p) {
-  using C = Cfg<BN, SWAP, QX, MX, PAIR>;
+template <bool GROUPED>
+using GemmParamsOf = std::conditional_t<GROUPED, GroupedGemmParams, GemmParams>;
+
+template <int BN, bool SWAP, bool OUT_F32, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
+__global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads,
+                                  Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kMinBlocks)
+    nvfp4_gemm_kernel(const __grid_constant__ GemmParamsOf<GROUPED> p) {
+  using C = Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -393,6 +502,17 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
   // can arrive on them
   if constexpr (PAIR) cluster_sync();
   const uint32_t tmem_base = *tmem_holder;
+  // grouped: the offsets come from an earlier kernel, and every address
+  // depends on them
+  const GroupTable* tab = reinterpret_cast<const GroupTable*>(smem + C::kOffTab);
+  if constexpr (GROUPED) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    load_groups<PAIR>(*reinterpret_cast<GroupTable*>(smem + C::kOffTab), p.offsets, p.E, p.M, p.err);
+  }
+  auto begin_work = [&]() {
+    if constexpr (GROUPED) return group_work_begin(p, SWAP, tab);
+    else return work_begin(p, SWAP, PAIR);
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -408,35 +528,59 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
       bool ok = true;
       // p0: this CTA's first row of P (CTA pairs: its 128-row half of the
       // 256-row tile); q0: the tile's first row of Q
-      auto for_steps = [&](WorkIter w, int first, int count, auto&& fn) {
+      auto for_steps = [&](auto w, int first, int count, auto&& fn) {
         int tp, tq, kb, ke, j = 0;
-        while (j < first + count && work_next(p, w, tp, tq, kb, ke))
+        while (j < first + count && work_next(p, w, tp, tq, kb, ke)) {
+          TileSrc t;
+          if constexpr (GROUPED && SWAP) {
+            t.p0 = w.g * (int)p.N + tp * kBM;
+            t.pb = w.g * p.w_blocks + tp;
+            t.q0 = w.row0;
+            t.qb = w.blk;
+            t.rows = w.rows;
+          } else if constexpr (GROUPED) {
+            t.p0 = w.row0 + (int)prank * kBM;
+            t.pb = w.blk + (int)prank;
+            t.q0 = w.g * (int)p.N + tq * BN;
+            t.qb = w.g * p.w_blocks + tq * 2;
+            t.rows = 0;
+          } else {
+            t.p0 = PAIR ? tp * 2 * kBM + (int)prank * kBM : tp * kBM;
+            t.pb = t.p0 >> 7;
+            t.q0 = tq * BN;
+            t.qb = t.q0 >> 7;
+            t.rows = 0;
+          }
           for (int k = kb; k < ke && j < first + count; ++k, ++j)
-            if (j >= first) fn(j, PAIR ? tp * 2 * kBM + (int)prank * kBM : tp * kBM, tq * BN, k);
+            if (j >= first) fn(j, t, k);
+        }
       };
-      auto nsfb_of = [&](int q0) {
+      // grouped, swapped: index of the box that holds the tile's rows
+      auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
+      auto nsfb_of = [&](const TileSrc& t) {
         int n = 0;
 #pragma unroll
         for (int rb = 0; rb < C::kSfbBlocks; ++rb)
-          if ((q0 >> 7) + rb < rb_q) ++n;
+          if (t.qb + rb < rb_q) ++n;
         return n;
       };
-      auto load_p = [&](int stage, int p0, int k) {
+      auto load_p = [&](int stage, const TileSrc& t, int k) {
+        const int p0 = t.p0;
         const uint32_t fb = bar_full + 8 * stage;
         const int nch = min(C::kChunks, kc - C::kChunks * k);
         if constexpr (PAIR) {
           // into this CTA's shared memory, completing on the even CTA's barrier
           tma_load_2d_pair(sbase + C::kOffA + stage * C::kABytes, &p.tmap_p, k * C::kRowBytes, p0, fb);
-          tma_load_2d_pair(sbase + C::kOffSfa + stage * C::kSfaBytes, &p.tmap_sfa, 0, (p0 >> 7) * kc + C::kChunks * k,
-                           fb);
+          tma_load_2d_pair(sbase + C::kOffSfa + stage * C::kSfaBytes, &p.tmap_sfa, 0, t.pb * kc + C::kChunks * k, fb);
           return;
         }
         tma_load_2d(sbase + C::kOffA + stage * C::kABytes, &p.tmap_p, k * C::kRowBytes, p0, fb);
-        size_t off = ((size_t)(p0 >> 7) * kc + C::kChunks * k) * kSfChunk;
+        size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
         if (!bounds_ok(off + (size_t)nch * kSfChunk <= p.sf_p_bytes, p.err)) off = 0;
         bulk_load(sbase + C::kOffSfa + stage * C::kSfaBytes, p.sf_p + off, (uint32_t)nch * kSfChunk, fb);
       };
-      auto load_q = [&](int stage, int q0, int k) {
+      auto load_q = [&](int stage, const TileSrc& t, int k) {
+        const int q0 = t.q0;
         const uint32_t fb = bar_full + 8 * stage;
         if constexpr (PAIR) {
           // this CTA's 128-row half of the weight tile, and the scales of all
@@ -446,22 +590,25 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
 #pragma unroll
           for (int rb = 0; rb < 2; ++rb)
             tma_load_2d_pair(sbase + C::kOffSfb + stage * C::kSfbBytes + rb * C::kChunks * kSfChunk, &p.tmap_sfb, 0,
-                             ((q0 >> 7) + rb) * kc + C::kChunks * k, fb);
+                             (t.qb + rb) * kc + C::kChunks * k, fb);
           return;
         }
         const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
-        const int nsfb = nsfb_of(q0);
-        tma_load_2d(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q, k * C::kRowBytes, q0, fb);
+        const int nsfb = nsfb_of(t);
+        if constexpr (GROUPED)
+          tma_load_2d(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q_box[box_of(t.rows)], k * C::kRowBytes, q0, fb);
+        else
+          tma_load_2d(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q, k * C::kRowBytes, q0, fb);
 #pragma unroll
         for (int rb = 0; rb < C::kSfbBlocks; ++rb)
           if (rb < nsfb) {
-            size_t off = ((size_t)((q0 >> 7) + rb) * kc + C::kChunks * k) * kSfChunk;
+            size_t off = ((size_t)(t.qb + rb) * kc + C::kChunks * k) * kSfChunk;
             if (!bounds_ok(off + sf_bytes <= p.sf_q_bytes, p.err)) off = 0;
             bulk_load(sbase + C::kOffSfb + stage * C::kSfbBytes + rb * C::kChunks * kSfChunk, p.sf_q + off, sf_bytes,
                       fb);
           }
       };
-      auto expect = [&](int stage, int q0, int k) {
+      auto expect = [&](int stage, const TileSrc& t, int k) {
         if constexpr (PAIR) {
           // the even CTA's barrier counts both CTAs' bytes (every box moves
           // its full size; rows past the tensor are zero-filled)
@@ -472,68 +619,71 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
         }
         const int nch = min(C::kChunks, kc - C::kChunks * k);
         const uint32_t sf_bytes = (uint32_t)nch * kSfChunk;
+        const uint32_t b_bytes = GROUPED ? (16u << box_of(t.rows)) * C::kRowBytes : C::kBBytes;
         mbar_arrive_expect_tx(bar_full + 8 * stage,
-                              C::kABytes + C::kBBytes + sf_bytes * (1 + (C::kQx ? 0 : nsfb_of(q0))));
+                              C::kABytes + b_bytes + sf_bytes * (1 + (C::kQx ? 0 : nsfb_of(t))));
       };
-      const WorkIter w0 = work_begin(p, SWAP, PAIR);
+      const auto w0 = begin_work();
       // prologue: the first kStages stages are free
       int npro = 0;
       const bool w_static = p.w_static != 0;
-      for_steps(w0, 0, C::kStages, [&](int j, int p0, int q0, int k) {
+      for_steps(w0, 0, C::kStages, [&](int j, const TileSrc& t, int k) {
+        npro = j + 1;
+        if constexpr (GROUPED) return;            // nothing to do before the wait: it is over
+        const int p0 = t.p0, q0 = t.q0;
         if (w_static) {
           // a weight declared read-only cannot be written by the preceding
           // kernel: load its first stages now
-          expect(j, q0, k);
-          if (SWAP) load_p(j, p0, k);
-          else load_q(j, q0, k);
+          expect(j, t, k);
+          if (SWAP) load_p(j, t, k);
+          else load_q(j, t, k);
           issued_mask |= 1u << j;
         } else {
           const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
           if (SWAP) {
             tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, p0);
-            const size_t off = ((size_t)(p0 >> 7) * kc + C::kChunks * k) * kSfChunk;
+            const size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
             if (bounds_ok(off + sf_bytes <= p.sf_p_bytes, p.err)) bulk_prefetch_l2(p.sf_p + off, sf_bytes);
           } else {
             tma_prefetch_l2_2d(&p.tmap_q, k * C::kRowBytes, PAIR ? q0 + (int)prank * kBM : q0);
           }
         }
-        npro = j + 1;
       });
-      if (SWAP) {
+      if (SWAP && !GROUPED) {
         // decode tiles stream each weight byte once: bring the rest of this
         // CTA's weight range into L2 now, so that HBM keeps streaming while
         // the preceding kernel finishes (a hint: it reads nothing into the CTA)
-        for_steps(w0, C::kStages, 1 << 30, [&](int, int p0, int, int k) {
+        for_steps(w0, C::kStages, 1 << 30, [&](int, const TileSrc& t, int k) {
           const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
-          tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, p0);
-          const size_t off = ((size_t)(p0 >> 7) * kc + C::kChunks * k) * kSfChunk;
+          tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, t.p0);
+          const size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
           if (bounds_ok(off + sf_bytes <= p.sf_p_bytes, p.err)) bulk_prefetch_l2(p.sf_p + off, sf_bytes);
         });
       }
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      for_steps(w0, 0, npro, [&](int j, int p0, int q0, int k) {
+      if constexpr (!GROUPED) asm volatile("griddepcontrol.wait;" ::: "memory");
+      for_steps(w0, 0, npro, [&](int j, const TileSrc& t, int k) {
         if (w_static) {
           if (SWAP) {
-            if (!C::kQx) load_q(j, q0, k);
+            if (!C::kQx) load_q(j, t, k);
           } else {
-            load_p(j, p0, k);
+            load_p(j, t, k);
           }
         } else {
-          expect(j, q0, k);
-          load_p(j, p0, k);
-          if (!C::kQx) load_q(j, q0, k);
+          expect(j, t, k);
+          load_p(j, t, k);
+          if (!C::kQx) load_q(j, t, k);
           issued_mask |= 1u << j;
         }
       });
       int stage = npro % C::kStages;
       uint32_t phase = npro == C::kStages ? 1u : 0u;
       if (npro == C::kStages) {
-        for_steps(w0, npro, 1 << 30, [&](int j, int p0, int q0, int k) {
+        for_steps(w0, npro, 1 << 30, [&](int j, const TileSrc& t, int k) {
           if (!ok) return;
           if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.err, p.timeout_ns)) { ok = false; return; }
-          expect(stage, q0, k);
-          load_p(stage, p0, k);
-          if (!C::kQx) load_q(stage, q0, k);
+          expect(stage, t, k);
+          load_p(stage, t, k);
+          if (!C::kQx) load_q(stage, t, k);
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         });
@@ -556,7 +706,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
     // ------------------------------------------------------------ MMA issuer
     // The whole warp follows the pipeline; lane 0 issues every MMA.  The copy
     // warps waited for each stage's data and moved its scales into TMEM.
-    constexpr uint32_t idesc = MX ? idesc_mxf4(C::kMmaM, BN) : idesc_nvf4(C::kMmaM, BN);
+    constexpr uint32_t idesc_full = MX ? idesc_mxf4(C::kMmaM, BN) : idesc_nvf4(C::kMmaM, BN);
     // Descriptors of stage 0, k-block 0; later stages and k-blocks only move
     // the 14-bit start-address field (address >> 4), which never carries.
     const uint64_t a_desc0 = smem_desc(sbase + C::kOffA, 16, C::kSbo, C::kSwizzleLayout);
@@ -565,12 +715,14 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
     int stage = 0, region = 0, lstep = 0;    // lstep: steps of this CTA so far
     uint32_t phase = 0, acc_phase = 0, acc_buf = 0;
     bool ok = true;
-    WorkIter w = work_begin(p, SWAP, PAIR);
+    auto w = begin_work();
     int tp, tq, kb0, ke0;
     // CTA pairs: only the even CTA issues (for both)
     while (ok && leader && work_next(p, w, tp, tq, kb0, ke0)) {
       if (!mbar_wait(bar_acc_empty, acc_phase ^ 1, abort_flag, p.err, p.timeout_ns)) break;
       tc_fence_after();
+      uint32_t idesc = idesc_full;
+      if constexpr (GROUPED && SWAP) idesc = idesc_nvf4(C::kMmaM, (w.rows + 15) & ~15);   // columns this tile has
       const uint32_t acc = tmem_base + (acc_buf ? C::kAcc1Col : 0);
       for (int k = kb0; k < ke0; ++k) {
         if (C::kQx && lstep >= C::kActSteps) {     // the host sizes the grid so this cannot happen
@@ -647,8 +799,12 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
     const bool tma_store = !SWAP && p.tma_store;
     uint32_t acc_phase = 0, acc_buf = 0;
     uint32_t out_buf = 0;                    // next staging buffer (TMA store path)
-    WorkIter w = work_begin(p, SWAP, PAIR);
-    const int64_t U = (int64_t)p.tiles_p * p.kt, G = gridDim.x;
+    auto w = begin_work();
+    int64_t U = (int64_t)p.tiles_p * p.kt, G = gridDim.x;
+    if constexpr (GROUPED) {
+      U = w.U;
+      G = w.G;
+    }
     int tp, tq, kb0, ke0;
     bool first_item = true;
     if constexpr (C::kQx) {
@@ -757,8 +913,24 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
     };
     while (work_next(p, w, tp, tq, kb0, ke0)) {
       // CTA pairs: this CTA's rows are its 128-row half of the 256-row tile
-      const int64_t p0 = PAIR ? (int64_t)tp * 2 * kBM + (int64_t)prank * kBM : (int64_t)tp * kBM;
-      const int64_t q0 = (int64_t)tq * BN;
+      int64_t p0 = PAIR ? (int64_t)tp * 2 * kBM + (int64_t)prank * kBM : (int64_t)tp * kBM;
+      int64_t q0 = (int64_t)tq * BN;
+      // first row past the tile's group (grouped), and whether this tile's
+      // rows go out through TMA stores, which write all 128 rows of a box
+      int64_t m_end = M;
+      bool tma_tile = tma_store;
+      float g_alpha = 0.0f;
+      if constexpr (GROUPED) {
+        if constexpr (SWAP) {
+          q0 = w.row0;
+          m_end = (int64_t)w.row0 + w.rows;
+        } else {
+          p0 = (int64_t)w.row0 + (int64_t)prank * kBM;
+          m_end = (int64_t)w.row0 + w.rows;
+          tma_tile = tma_store && p0 + kBM <= m_end;
+        }
+        g_alpha = (float)(1.0 / ((double)__ldg(p.ga + w.g) * (double)__ldg(p.gw + w.g)));
+      }
       if (!mbar_wait(bar_acc_full, acc_phase, abort_flag, p.err, p.timeout_ns)) break;
       __syncwarp();
       tc_fence_after();
@@ -785,12 +957,12 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
             // one scale for the whole 64-column slot unless a segment
             // boundary falls inside it
             int seg_lo = 0, seg_hi = 0;
-            if (n_seg > 1) {
+            if (!GROUPED && n_seg > 1) {
               seg_lo = seg_index_smem(seg_end_s, n_seg, n0);
               seg_hi = seg_index_smem(seg_end_s, n_seg, n0 + 63 < N ? n0 + 63 : N - 1);
             }
-            if (seg_lo == seg_hi) {
-              const float a = seg_alpha_s[seg_lo];
+            if (GROUPED || seg_lo == seg_hi) {
+              const float a = GROUPED ? g_alpha : seg_alpha_s[seg_lo];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 packed[slot * 32 + i] = pack_bf16x2(__fmul_rn(__uint_as_float(r0[2 * i]), a),
@@ -815,7 +987,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
             }
           }
           if (!C::kOverlapAcc) release_acc();
-          if (tma_store) {
+          if (tma_tile) {
             // 64-column sub-tiles through two 16 KB swizzled staging buffers
 #pragma unroll
             for (int sub = 0; sub < BN / 64; ++sub) {
@@ -842,11 +1014,20 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
               }
               out_buf ^= 1;
             }
-          } else if (m < M) {
+          } else if (m < m_end) {
             __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) + m * N;
 #pragma unroll
             for (int c = 0; c < BN / 8; ++c) {
               const int64_t n = q0 + slot_col(c / 8) + (c % 8) * 8;
+              if constexpr (GROUPED) {
+                // the last rows of a group: 16-byte stores where rows allow them
+                if (tma_store && n + 8 <= N) {
+                  if (bounds_ok((uint64_t)(m * N + n + 8) <= p.out_elems, p.err))
+                    *reinterpret_cast<uint4*>(orow + n) =
+                        make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
+                  continue;
+                }
+              }
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (n + e < N && bounds_ok((uint64_t)(m * N + n + e) < p.out_elems, p.err))
@@ -866,12 +1047,12 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
             if (cc == 2 * C::kSharedSlots - 1 && C::kOverlapAcc) release_acc();
             const int64_t n0 = q0 + c * 32;
             int seg_lo = 0, seg_hi = 0;
-            if (n_seg > 1) {
+            if (!GROUPED && n_seg > 1) {
               seg_lo = seg_index_smem(seg_end_s, n_seg, n0);
               seg_hi = seg_index_smem(seg_end_s, n_seg, n0 + 31 < N ? n0 + 31 : N - 1);
             }
-            if (seg_lo == seg_hi) {
-              const float a = seg_alpha_s[seg_lo];
+            if (GROUPED || seg_lo == seg_hi) {
+              const float a = GROUPED ? g_alpha : seg_alpha_s[seg_lo];
 #pragma unroll
               for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), a));
             } else {
@@ -880,7 +1061,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
                 r[i] = __float_as_uint(
                     __fmul_rn(__uint_as_float(r[i]), seg_alpha_smem(seg_end_s, seg_alpha_s, n_seg, n0 + i)));
             }
-            if (tma_store && q0 + c * 32 < N) {
+            if (tma_tile && q0 + c * 32 < N) {
               const uint32_t buf = sbase + C::kOffOut + out_buf * kStageOutBytes;
               if (et == 0) bulk_wait_group_read<1>();
               named_bar_sync(kEpiBar, 128);
@@ -896,11 +1077,18 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
                 bulk_commit_group();
               }
               out_buf ^= 1;
-            } else if (!tma_store && m < M) {
+            } else if (!tma_tile && m < m_end) {
               float* orow = reinterpret_cast<float*>(p.out) + m * N;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const int64_t n = q0 + c * 32 + i;
+                if constexpr (GROUPED) {
+                  if (tma_store && n - (i & 3) + 4 <= N) {
+                    if ((i & 3) == 0 && bounds_ok((uint64_t)(m * N + n + 4) <= p.out_elems, p.err))
+                      *reinterpret_cast<uint4*>(orow + n) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+                    continue;
+                  }
+                }
                 if (n < N && bounds_ok((uint64_t)(m * N + n) < p.out_elems, p.err)) orow[n] = __uint_as_float(r[i]);
               }
             }
@@ -912,11 +1100,12 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
         // activation row.  The whole accumulator row goes to registers, then
         // TMEM is handed back.
         const int64_t n = p0 + row;
-        const float alpha = seg_alpha_smem(seg_end_s, seg_alpha_s, n_seg, n);
+        const float alpha = GROUPED ? g_alpha : seg_alpha_smem(seg_end_s, seg_alpha_s, n_seg, n);
         constexpr int kCols = BN < 32 ? BN : 32;
         uint32_t r[(BN + 31) / 32][kCols];
 #pragma unroll
         for (int c = 0; c < (BN + 31) / 32; ++c) {
+          if (GROUPED && q0 + c * 32 >= m_end) break;
           if constexpr (BN >= 32) {
             tmem_ld_32x32b_x32(taddr + c * 32, r[c]);
           } else {
@@ -937,19 +1126,22 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
           if constexpr (OUT_F32) reinterpret_cast<float*>(p.out)[mm * N + n] = v;
           else reinterpret_cast<__nv_bfloat16*>(p.out)[mm * N + n] = __float2bfloat16_rn(v);
         };
-        const int64_t tile_u0 = (int64_t)tp * p.kt;
+        int64_t tile_u0 = (int64_t)tp * p.kt;
+        if constexpr (GROUPED) tile_u0 = w.tile * p.kt;
         const int64_t c_first = cta_of_unit(tile_u0, U, G);
         const int64_t c_last = cta_of_unit(tile_u0 + p.kt - 1, U, G);
         if (c_first == c_last) {
           // the whole K range of this tile ran here
           if (n < N) {
 #pragma unroll
-            for (int c = 0; c < (BN + 31) / 32; ++c)
+            for (int c = 0; c < (BN + 31) / 32; ++c) {
+              if (GROUPED && q0 + c * 32 >= m_end) break;
 #pragma unroll
               for (int i = 0; i < kCols; ++i) {
                 const int64_t mm = q0 + c * 32 + i;
-                if (mm < M) store_out(mm, __fmul_rn(__uint_as_float(r[c][i]), alpha));
+                if (mm < m_end) store_out(mm, __fmul_rn(__uint_as_float(r[c][i]), alpha));
               }
+            }
           }
         } else {
           // split tile.  The CTA that holds the tile's first K steps (its last
@@ -965,13 +1157,15 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
             const int64_t part0 = (2 * (int64_t)blockIdx.x + (first_item ? 0 : 1)) * BN * kBM + row;
             uint64_t* part = p.ws + part0;
 #pragma unroll
-            for (int c = 0; c < (BN + 31) / 32; ++c)
+            for (int c = 0; c < (BN + 31) / 32; ++c) {
+              if (GROUPED && q0 + c * 32 >= m_end) break;
 #pragma unroll
               for (int i = 0; i < kCols; ++i) {
                 const int mm = c * 32 + i;
-                if (q0 + mm < M && bounds_ok((uint64_t)(part0 + (int64_t)mm * kBM) < p.ws_words, p.err))
+                if (q0 + mm < m_end && bounds_ok((uint64_t)(part0 + (int64_t)mm * kBM) < p.ws_words, p.err))
                   st_full_word(part + (int64_t)mm * kBM, r[c][i]);
               }
+            }
           } else {
             float sum[(BN + 31) / 32][kCols];
 #pragma unroll
@@ -990,13 +1184,14 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
               // one round polls every word of a 32-column chunk at once
 #pragma unroll
               for (int cb = 0; cb < (BN + 31) / 32; ++cb) {
+                if (GROUPED && q0 + cb * 32 >= m_end) break;
                 uint64_t v[kCols];
                 const uint64_t t0 = globaltimer_ns();
                 while (true) {
 #pragma unroll
                   for (int i = 0; i < kCols; ++i) {
                     const int mm = cb * 32 + i;
-                    v[i] = q0 + mm < M ? ld_word(src + (int64_t)mm * kBM) : (uint64_t)kFullTag << 32;
+                    v[i] = q0 + mm < m_end ? ld_word(src + (int64_t)mm * kBM) : (uint64_t)kFullTag << 32;
                   }
                   uint32_t all = p.test_stall ? 0u : 1u;
 #pragma unroll
@@ -1013,18 +1208,20 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
                 for (int i = 0; i < kCols; ++i) {
                   const int mm = cb * 32 + i;
                   sum[cb][i] = __fadd_rn(sum[cb][i], __uint_as_float((uint32_t)v[i]));
-                  if (q0 + mm < M) st_word(src + (int64_t)mm * kBM, 0ull);     // empty again
+                  if (q0 + mm < m_end) st_word(src + (int64_t)mm * kBM, 0ull);     // empty again
                 }
               }
             }
             if (n < N && ok_all) {
 #pragma unroll
-              for (int cb = 0; cb < (BN + 31) / 32; ++cb)
+              for (int cb = 0; cb < (BN + 31) / 32; ++cb) {
+                if (GROUPED && q0 + cb * 32 >= m_end) break;
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) {
                   const int64_t mm = q0 + cb * 32 + i;
-                  if (mm < M) store_out(mm, __fmul_rn(sum[cb][i], alpha));
+                  if (mm < m_end) store_out(mm, __fmul_rn(sum[cb][i], alpha));
                 }
+              }
             }
           }
         }
@@ -1051,7 +1248,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR>::kThreads, Cfg<BN,
       int64_t step = 0;                         // pipeline steps issued so far
       uint32_t phase = 0;
       bool ok = true;
-      WorkIter w = work_begin(p, SWAP, PAIR);
+      auto w = begin_work();
       int tp, tq, kb0, ke0;
       while (ok && work_next(p, w, tp, tq, kb0, ke0)) {
         for (int k = kb0; k < ke0; ++k) {

@@ -1,0 +1,303 @@
+// W4A4 linear layer over experts: the grouped activation quantizer and the
+// grouped GEMM.
+//
+//   quantize  row t of group g = NVFP4(x[row_index[t]], gs[g]), or of
+//             silu(gate) * up of a row [gate | up]
+//   gemm      out[t, n] = 1 / (ga[g] gw[g]) * sum_k A[t, k] W_g[n, k]
+//
+// Group offsets live on the device (the router wrote them), so both kernels
+// build the table of groups.cuh in shared memory and take their work from it.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "block_quant.cuh"
+#include "common.h"
+#include "gemm_host.h"
+#include "gemm_kernel.cuh"
+#include "groups.cuh"
+#include "ptx.cuh"
+
+namespace nvfp4 {
+
+struct GroupedQuantParams {
+  const void* x;
+  int64_t M;                  // rows of x
+  const int32_t* row_index;   // or NULL: row t of x
+  const int32_t* offsets;
+  int E;
+  int64_t T;
+  uint32_t nblk;              // K / 16
+  DivU32 div_nblk;
+  const float* gs;
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t kc;
+  uint64_t codes_bytes, scale_bytes;
+  unsigned* err;
+};
+
+// One thread owns one 16-element block, as in the plain quantizer; a CTA owns
+// a contiguous share of the blocks of all rows that the offsets name, so that
+// it builds the group table once and a thread's group only moves forward.
+// Memory-bound: each source row is read once from HBM (repeats of a gathered
+// row hit L2) and 9/16 byte an element written.
+template <bool kF32, bool kGlu>
+__global__ void __launch_bounds__(256) grouped_quantize_kernel(const GroupedQuantParams p) {
+  __shared__ GroupTable tab;
+  constexpr int U = 2;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  load_groups(tab, p.offsets, p.E, p.T, p.err);
+  const uint64_t total = (uint64_t)tab.off[p.E] * p.nblk;
+  const uint32_t b_begin = (uint32_t)(total * blockIdx.x / gridDim.x);
+  const uint32_t b_end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
+  if (b_begin >= b_end) return;
+  const int64_t src_stride = (int64_t)p.nblk * (kGlu ? 2 : 1);      // source row, in blocks
+  int g = find_group(tab.off, p.E, (int)div_u32(b_begin, p.div_nblk));
+  float gs = __ldg(p.gs + g);
+  for (uint32_t base = b_begin + threadIdx.x; base < b_end; base += U * 256) {
+    Block16<kF32> B[U], C[kGlu ? U : 1];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t b = base + u * 256;
+      if (b >= b_end) break;
+      const uint32_t row = div_u32(b, p.div_nblk);
+      const uint32_t j = b - row * p.nblk;
+      int64_t src = row;
+      if (p.row_index) src = __ldg(p.row_index + row);
+      B[u] = Block16<kF32>{};
+      if constexpr (kGlu) C[u] = Block16<kF32>{};
+      if (src >= 0 && src < p.M) {
+        const uint8_t* q = reinterpret_cast<const uint8_t*>(p.x) + (src * src_stride + j) * (kF32 ? 64 : 32);
+        load_block_at<kF32>(q, B[u]);
+        if constexpr (kGlu) load_block_at<kF32>(q + (int64_t)p.nblk * (kF32 ? 64 : 32), C[u]);
+      } else {
+        atomicCAS(p.err, 0u, kErrBounds);       // a row that x does not have: quantized as zeros
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t b = base + u * 256;
+      if (b >= b_end) break;
+      const uint32_t row = div_u32(b, p.div_nblk);
+      const uint32_t j = b - row * p.nblk;
+      if ((int)row >= tab.off[g + 1]) {
+        do ++g;
+        while ((int)row >= tab.off[g + 1]);
+        gs = __ldg(p.gs + g);
+      }
+      float f[16], amax;
+      block_floats<kF32>(B[u], f);
+      if constexpr (kGlu) {
+        float up[16];
+        block_floats<kF32>(C[u], up);
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          f[i] = f[i] * __frcp_rn(1.0f + expf(-f[i])) * up[i];
+          amax = fmaxf(amax, fabsf(f[i]));
+        }
+      } else {
+        amax = block_amax<kF32>(B[u]);
+      }
+      uint32_t lo, hi;
+      const uint32_t s = quantize_values(f, amax, gs, lo, hi);
+      if (bounds_ok((uint64_t)(b + 1) * 8 <= p.codes_bytes, p.err))
+        reinterpret_cast<uint2*>(p.codes)[b] = make_uint2(lo, hi);
+      const int64_t pos = (int64_t)tab.blk[g] * 128 + ((int)row - tab.off[g]);
+      const int64_t o = tc_scale_offset(pos, j, p.kc);
+      if (bounds_ok((uint64_t)o < p.scale_bytes, p.err)) p.scales[o] = (uint8_t)s;
+      // K % 64 == 32: the row's last chunk has two padding slots
+      if (j == p.nblk - 1 && (p.nblk & 3) == 2) {
+        const int64_t o2 = tc_scale_offset(pos, j + 2, p.kc);
+        if (bounds_ok((uint64_t)o2 < p.scale_bytes, p.err)) {
+          p.scales[o2 - 1] = 0;
+          p.scales[o2] = 0;
+        }
+      }
+    }
+  }
+}
+
+namespace {
+
+// Which tiles multiply: swapped tiles (128 weight rows by up to 128
+// activation rows, K split over the CTAs) stream each expert's weight once
+// and waste nothing on groups of a few rows; CTA pairs (256 x 256) reach the
+// tensor cores' rate once groups fill them.  The host knows only the mean
+// rows of a group.
+bool grouped_swap(int64_t T, int64_t E) { return T < 192 * E; }
+
+nvfp4_status run_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* ga, const uint8_t* w_codes,
+                              const uint8_t* w_scales, const float* gw, const int32_t* offsets, int E, int64_t T,
+                              int64_t N, int64_t K, void* out, bool f32, void* workspace, size_t workspace_bytes,
+                              const DeviceInfo* d, cudaStream_t st) {
+  GroupedGemmParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.err = d->err_word;
+  p.timeout_ns = wait_timeout_ns();
+  p.drain_ns = drain_timeout_ns();
+  p.M = T;
+  p.N = N;
+  p.offsets = offsets;
+  p.ga = ga;
+  p.gw = gw;
+  p.E = E;
+  p.w_blocks = (int)ceil_div(N, 128);
+  p.kc = (int)ceil_div(K, 64);
+  p.kmma = p.kc;
+  p.out = out;
+  p.out_elems = (uint64_t)T * (uint64_t)N;
+  const int64_t a_blocks = grouped_blocks(T, E), w_blocks = (int64_t)E * p.w_blocks;
+  const uint64_t a_sf = (uint64_t)a_blocks * p.kc * kSfChunk, w_sf = (uint64_t)w_blocks * p.kc * kSfChunk;
+  const bool swap = grouped_swap(T, E);
+  if (swap) {
+    using Cf = Cfg<128, true, 0, false, false, true>;
+    if (workspace) {
+      if (workspace_bytes < workspace_need(d, 128)) return NVFP4_ERR_INVALID_ARG;
+      p.ws = static_cast<uint64_t*>(workspace);
+      p.ws_words = workspace_bytes / sizeof(uint64_t);
+    } else {
+      Workspace w;
+      const cudaError_t e = get_workspace(d, st, 128, &w);
+      if (e == cudaErrorNotPermitted) return NVFP4_ERR_UNSUPPORTED;
+      if (e == cudaErrorInvalidValue) return NVFP4_ERR_INVALID_ARG;
+      if (e != cudaSuccess) return cuda_status(e);
+      p.ws = w.ws;
+      p.ws_words = w.bytes / sizeof(uint64_t);
+    }
+    p.rows_p = (int)(E * N);
+    p.rows_q = (int)T;
+    p.sf_p = w_scales;
+    p.sf_q = a_scales;
+    p.sf_p_bytes = w_sf;
+    p.sf_q_bytes = a_sf;
+    p.rb_q = (int)a_blocks;
+    p.kt = (int)ceil_div(K, 64 * Cf::kKB);
+    p.tiles_p = p.w_blocks;
+    if (!make_code_map(&p.tmap_p, w_codes, p.rows_p, K, kBM, Cf::kRowBytes)) return NVFP4_ERR_CUDA;
+    for (int i = 0; i < 4; ++i)
+      if (!make_code_map(&p.tmap_q_box[i], a_codes, T, K, 16 << i, Cf::kRowBytes)) return NVFP4_ERR_CUDA;
+    p.tmap_q = p.tmap_q_box[3];
+    const cudaError_t e = f32 ? launch<128, true, true, 0, false, false, true>(p, d, st, d->sm_count)
+                              : launch<128, true, false, 0, false, false, true>(p, d, st, d->sm_count);
+    return cuda_status(e);
+  }
+  using Cf = Cfg<256, false, 0, false, true, true>;
+  p.rows_p = (int)T;
+  p.rows_q = (int)(E * N);
+  p.sf_p = a_scales;
+  p.sf_q = w_scales;
+  p.sf_p_bytes = a_sf;
+  p.sf_q_bytes = w_sf;
+  p.rb_q = (int)w_blocks;
+  p.kt = (int)ceil_div(K, 64 * Cf::kKB);
+  p.tiles_q = (int)ceil_div(N, 256);
+  p.group_p = Cf::kGroupTiles;
+  p.tma_store = (N * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;
+  if (!make_code_map(&p.tmap_p, a_codes, T, K, kBM, Cf::kRowBytes) ||
+      !make_code_map(&p.tmap_q, w_codes, p.rows_q, K, kBM, Cf::kRowBytes) ||
+      !make_sf_map(&p.tmap_sfa, a_scales, a_blocks * 128, p.kc, Cf::kChunks) ||
+      !make_sf_map(&p.tmap_sfb, w_scales, w_blocks * 128, p.kc, Cf::kChunks) ||
+      (p.tma_store && !make_out_map(&p.tmap_out, out, T, N, f32)))
+    return NVFP4_ERR_CUDA;
+  const int grid = d->sm_count / 2 * 2;
+  const cudaError_t e = f32 ? launch<256, false, true, 0, false, true, true>(p, d, st, grid, 2)
+                            : launch<256, false, false, 0, false, true, true>(p, d, st, grid, 2);
+  return cuda_status(e);
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+size_t nvfp4_grouped_scale_bytes(int64_t T, int n_groups, int64_t K) {
+  if (T < 1 || n_groups < 1 || n_groups > NVFP4_MAX_GROUPS || K < 16 || K % 16 != 0) return 0;
+  return (size_t)(grouped_blocks(T, n_groups) * ceil_div(K, 64) * 512);
+}
+
+nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_act act, int64_t M, int64_t K,
+                                    const int32_t* row_index, const int32_t* group_offsets, int n_groups, int64_t T,
+                                    const float* global_scales, uint8_t* codes, uint8_t* block_scales,
+                                    nvfp4_stream_t stream) {
+  if (!x || !group_offsets || !global_scales || !codes || !block_scales) return NVFP4_ERR_INVALID_ARG;
+  if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
+  if (act != NVFP4_ACT_NONE && act != NVFP4_ACT_SWIGLU) return NVFP4_ERR_INVALID_ARG;
+  if (M < 1 || T < 1 || K < 32 || K % 32 != 0 || n_groups < 1) return NVFP4_ERR_INVALID_ARG;
+  if (!row_index && M < T) return NVFP4_ERR_INVALID_ARG;
+  if (n_groups > NVFP4_MAX_GROUPS || T > (1ll << 31) - 256 || M > (1ll << 31) - 256 || K > (1ll << 31) ||
+      T * (K / 16) >= (1ll << 31) - (1ll << 20))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(block_scales)) return NVFP4_ERR_ALIGNMENT;
+  if (!aligned4(row_index) || !aligned4(group_offsets) || !aligned4(global_scales)) return NVFP4_ERR_ALIGNMENT;
+  const DeviceInfo* d = device_info();
+  if (!d) return NVFP4_ERR_CUDA;
+  if (d->major != 10) return NVFP4_ERR_UNSUPPORTED;
+  GroupedQuantParams p;
+  p.x = x;
+  p.M = M;
+  p.row_index = row_index;
+  p.offsets = group_offsets;
+  p.E = n_groups;
+  p.T = T;
+  p.nblk = (uint32_t)(K / 16);
+  p.div_nblk = make_div(p.nblk);
+  p.gs = global_scales;
+  p.codes = codes;
+  p.scales = block_scales;
+  p.kc = ceil_div(K, 64);
+  p.codes_bytes = (uint64_t)T * (uint64_t)(K / 2);
+  p.scale_bytes = nvfp4_grouped_scale_bytes(T, n_groups, K);
+  p.err = d->err_word;
+  const int64_t want = ceil_div(T * (K / 16), 256);
+  const int64_t cap = (int64_t)d->sm_count * 8;
+  const int grid = (int)(want < cap ? want : cap);
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool f32 = dtype == NVFP4_IN_F32, glu = act == NVFP4_ACT_SWIGLU;
+  cudaError_t e;
+  if (f32) e = glu ? launch_pdl(grouped_quantize_kernel<true, true>, grid, 256, st, p)
+                   : launch_pdl(grouped_quantize_kernel<true, false>, grid, 256, st, p);
+  else e = glu ? launch_pdl(grouped_quantize_kernel<false, true>, grid, 256, st, p)
+               : launch_pdl(grouped_quantize_kernel<false, false>, grid, 256, st, p);
+  return cuda_status(e);
+}
+
+size_t nvfp4_grouped_workspace_bytes(int64_t T, int n_groups) {
+  if (T < 1 || n_groups < 1 || n_groups > NVFP4_MAX_GROUPS || !grouped_swap(T, n_groups)) return 0;
+  const DeviceInfo* d = device_info();
+  return d ? workspace_need(d, 128) : 0;
+}
+
+nvfp4_status nvfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_global_scales,
+                                const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scales,
+                                const int32_t* group_offsets, int n_groups, int64_t T, int64_t N, int64_t K, void* out,
+                                nvfp4_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                nvfp4_stream_t stream) {
+  if (!a_codes || !a_scales || !a_global_scales || !w_codes || !w_scales || !w_global_scales || !group_offsets || !out)
+    return NVFP4_ERR_INVALID_ARG;
+  if (T < 1 || N < 1 || K < 32 || K % 32 != 0 || n_groups < 1) return NVFP4_ERR_INVALID_ARG;
+  if (out_dtype != NVFP4_OUT_BF16 && out_dtype != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
+  if (!workspace && workspace_bytes != 0) return NVFP4_ERR_INVALID_ARG;
+  // coordinates of the stacked weight and of its scale chunks, and tile
+  // counts, are 32-bit
+  const int64_t lim = (1ll << 31) - 65536;
+  if (n_groups > NVFP4_MAX_GROUPS || T > lim || N > lim / n_groups || K > lim ||
+      (int64_t)n_groups * ceil_div(N, 128) > lim / ceil_div(K, 64) ||
+      grouped_blocks(T, n_groups) > lim / ceil_div(K, 64) || grouped_blocks(T, n_groups) > lim / ceil_div(N, 128))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(out) ||
+      !aligned16(workspace))
+    return NVFP4_ERR_ALIGNMENT;
+  if (!aligned4(a_global_scales) || !aligned4(w_global_scales) || !aligned4(group_offsets)) return NVFP4_ERR_ALIGNMENT;
+  const DeviceInfo* d = device_info();
+  if (!d) return NVFP4_ERR_CUDA;
+  if (d->major != 10) return NVFP4_ERR_UNSUPPORTED;
+  return run_grouped_gemm(a_codes, a_scales, a_global_scales, w_codes, w_scales, w_global_scales, group_offsets,
+                          n_groups, T, N, K, out, out_dtype == NVFP4_OUT_F32, workspace, workspace_bytes, d,
+                          (cudaStream_t)stream);
+}
+
+}  // extern "C"

@@ -20,11 +20,6 @@
 
 namespace nvfp4 {
 
-// Offset of scale j of row r in the tensor-core scale layout.
-__device__ __forceinline__ int64_t tc_scale_offset(int64_t r, int64_t j, int64_t kc) {
-  return ((r >> 7) * kc + (j >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (j & 3);
-}
-
 // Raise *amax to v.  Non-negative floats order like their bit patterns, so
 // an unsigned atomic maximum does it; the word only grows while the kernel
 // runs, so a CTA whose maximum is not above a value it reads there has
