@@ -504,28 +504,18 @@ NVFP4_API nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtyp
  *   w_codes  device [n_groups, N, K/2]; w_scales device, n_groups consecutive
  *            TCGEN05 buffers of nvfp4_scale_bytes(N, K, TCGEN05) bytes
  *   out      device [T, N] row-major; rows outside the groups left as they were
- *   workspace, workspace_bytes: device, 16-byte aligned, at least
- *            nvfp4_grouped_workspace_bytes(T, n_groups) bytes, zero-filled
- *            before its first use (each launch leaves it zero again); or NULL
- *            and 0 to use the K-split workspace of the stream, under the rules
- *            and the capture restriction of nvfp4_gemm.  Two graphs captured
- *            on one stream that may be replayed at the same time share that
- *            workspace and would race on it: give each its own.
- * A mean of fewer than 192 rows a group (T / n_groups) runs weight-streaming
- * tiles whose K loop is split over the CTAs: progress and the bounded waits as
- * nvfp4_gemm describes for 16 < M <= 128, nvfp4_set_decode_cooperative
- * included; the partial sums are added in a fixed order.  More rows run as
- * 256 x 256 CTA-pair tiles without a workspace.
+ * Tiles of 256 weight rows by up to 128 (T / n_groups < 128) or 256 rows of
+ * one group, without a workspace: calls on different streams share nothing,
+ * and no CTA waits for another one's result (but for the two of a pair).  The
+ * result does not depend on timing.
  * Codes, scales and out 16-byte aligned, the other pointers 4-byte.
  * Errors: INVALID_ARG, UNSUPPORTED (not sm_100, too many groups,
- * n_groups * N >= 2^31 - 65536, a first call during capture with no
- * workspace), ALIGNMENT, CUDA. */
-NVFP4_API size_t nvfp4_grouped_workspace_bytes(int64_t T, int n_groups);
+ * n_groups * N >= 2^31 - 65536, or (T / 128 + n_groups) * N / 256
+ * >= 2^30), ALIGNMENT, CUDA. */
 NVFP4_API nvfp4_status nvfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_global_scales,
                                 const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scales,
                                 const int32_t* group_offsets, int n_groups, int64_t T, int64_t N, int64_t K, void* out,
-                                nvfp4_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                                nvfp4_stream_t stream);
+                                nvfp4_out_dtype out_dtype, nvfp4_stream_t stream);
 
 /* Block norm: the step between two linear layers of a block, for rows m < M:
  *   b = y[m], or with slots  sum_j slot_weights[m, j] * y[slots[m, j]]

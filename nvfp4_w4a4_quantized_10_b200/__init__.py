@@ -81,10 +81,8 @@ _lib.nvfp4_grouped_scale_bytes.restype = ctypes.c_size_t
 _lib.nvfp4_grouped_scale_bytes.argtypes = [_i64, ctypes.c_int, _i64]
 _lib.nvfp4_grouped_quantize.argtypes = [_vp, ctypes.c_int, ctypes.c_int, _i64, _i64, _vp, _vp, ctypes.c_int, _i64, _vp,
                                         _vp, _vp, _vp]
-_lib.nvfp4_grouped_workspace_bytes.restype = ctypes.c_size_t
-_lib.nvfp4_grouped_workspace_bytes.argtypes = [_i64, ctypes.c_int]
 _lib.nvfp4_grouped_gemm.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp,
-                                    ctypes.c_int, _vp, ctypes.c_size_t, _vp]
+                                    ctypes.c_int, _vp]
 _lib.nvfp4_block_norm.argtypes = [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, ctypes.c_int, _vp, _i64, _vp,
                                   ctypes.c_int, _vp, _f32, _vp, _vp, _f32, _vp, _vp, _vp, _f32, ctypes.c_int, _vp]
 _lib.nvfp4_convert_e4m3.argtypes = [_vp, _vp, _i64, _vp]
@@ -386,13 +384,9 @@ def nvfp4_grouped_quantize(x: torch.Tensor, group_offsets: torch.Tensor, global_
                                            _stream(x)))
 
 
-def nvfp4_grouped_workspace_bytes(T: int, n_groups: int) -> int:
-    return int(_lib.nvfp4_grouped_workspace_bytes(T, n_groups))
-
-
 def nvfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scales: torch.Tensor,
                        w_codes: torch.Tensor, w_scales: torch.Tensor, w_global_scales: torch.Tensor,
-                       group_offsets: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor | None = None) -> None:
+                       group_offsets: torch.Tensor, out: torch.Tensor) -> None:
     """a_codes [T, K/2] with grouped scales times w_codes [E, N, K/2] (scales:
     E TCGEN05 buffers) -> out [T, N]."""
     T, K = a_codes.shape[0], 2 * a_codes.shape[1]
@@ -409,9 +403,7 @@ def nvfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_s
                                        _room("w_scales", w_scales, E * nvfp4_scale_bytes(N, K), dev),
                                        _typed("w_global_scales", w_global_scales, f32, (E,), dev),
                                        _typed("group_offsets", group_offsets, torch.int32, (E + 1,), dev), E, T, N, K,
-                                       _ptr(out), _out_dtype(out), _room("workspace", workspace, 0, dev),
-                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                       _stream(out)))
+                                       _ptr(out), _out_dtype(out), _stream(out)))
 
 
 def nvfp4_block_norm(y: torch.Tensor, slots: torch.Tensor | None = None, slot_weights: torch.Tensor | None = None,

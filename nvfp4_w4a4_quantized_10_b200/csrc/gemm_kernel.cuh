@@ -54,6 +54,7 @@ constexpr int kSfChunk = 512;     // bytes of one 128-row x 4-scale chunk
 constexpr int kTmemCols = 512;
 constexpr int kGroupP = 64;       // tile raster: 64 P-tiles (8192 rows) share each Q-tile sweep
 constexpr int kStageOutBytes = 16384;   // one 128-row x 128-byte output sub-tile
+constexpr int kTileSlots = 16;    // grouped GEMM: ring of tile numbers
 constexpr int kEpiBar = 1;        // named barrier id of the 128 epilogue threads
 
 struct alignas(64) GemmParams {
@@ -99,7 +100,7 @@ struct alignas(64) GemmParams {
 // activation rows of group g are [off[g], off[g + 1]), its weight rows
 // [g N, (g + 1) N) of one [E N, K / 2] operand.
 struct GroupedGemmParams : GemmParams {
-  CUtensorMap tmap_q_box[4];   // swapped tiles: activation codes in boxes of 16, 32, 64 and 128 rows
+  CUtensorMap tmap_q_box[4];   // activation codes in boxes of 16, 32, 64 and 128 rows
   const int32_t* offsets;      // device [E + 1]
   const float* ga;             // device [E], activation and weight global scales
   const float* gw;
@@ -119,10 +120,14 @@ struct GroupedGemmParams : GemmParams {
 // scale copies for both (tcgen05 cta_group::2); each CTA drains its own 128
 // accumulator rows.
 // GROUPED: the rows are split into groups (experts), each multiplied by a
-// weight of its own; group offsets are read on the device.  Swapped tiles
-// then have up to BN = 128 activation rows of one group, and load and
-// multiply only as many (rounded up to a box of 16, 32, 64 or 128 rows, and
-// to 16 columns of the MMA); CTA-pair tiles never cross a group.
+// weight of its own; group offsets are read on the device.  CTA pairs put the
+// weight on P, 128 rows a CTA, and up to BN activation rows of one group on
+// Q: the MMA's N is as many columns as the tile has rows (rounded up to 32),
+// so a group's last tile costs what its rows cost, and each CTA loads its half
+// of them in the smallest of four boxes (16, 32, 64, 128 rows).  With the
+// activations on P, whose 256 rows are fixed, 32768 rows in 64 groups against
+// weights of 2048 x 5120 took 237 us instead of 219.  BN = 256 for large
+// groups; BN = 128 leaves room for more stages, and two whole accumulators.
 template <int BN, bool SWAP, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
 struct Cfg {
   static constexpr bool kQx = QX != 0;
@@ -154,7 +159,7 @@ struct Cfg {
   // CTA pairs keep 4 stages although 5 fit: 5 ran 2-7 % slower on every
   // prefill and fused shape measured (the deeper ring lets the copy warps
   // run further ahead of MMAs that are not waiting on data)
-  static constexpr int kMaxStages = PAIR ? 4 : 8;
+  static constexpr int kMaxStages = PAIR && BN == 256 ? 4 : 8;
   // Decode tiles with a small activation side keep to under half of the
   // SM's shared memory (and TMEM, and 128 registers), so two CTAs fit on an
   // SM.  With BN = 16 the grid has 2 x SMs CTAs: each streams half as much
@@ -199,7 +204,10 @@ struct Cfg {
   static constexpr int kOffMisc = kOffSeg + 2 * 4 * NVFP4_MAX_SEGMENTS;
   static constexpr int kOffRtab = kOffMisc + 16;                     // in-kernel activation: g / e4m3(s)
   static constexpr int kOffTab = kOffRtab + (kQx ? 1024 : 0);        // grouped: table of groups
-  static constexpr int kSmemBytes = kOffTab + (GROUPED ? (int)sizeof(GroupTable) : 0) + 1024;   // + alignment slack
+  // grouped: the answer to a work request and its barrier, the ring of tile
+  // numbers and its barriers
+  static constexpr int kOffClc = (kOffTab + (GROUPED ? (int)sizeof(GroupTable) : 0) + 15) / 16 * 16;
+  static constexpr int kSmemBytes = kOffClc + (GROUPED ? 16 + 8 + kTileSlots * (8 + 4) : 0) + 1024;   // + alignment slack
   // TMEM columns.  Normal 128x256 tiles: the copy warps run ahead of the
   // MMAs, so the scales of successive steps use a ring of regions at the top
   // of TMEM ([320,512) for four 48-column regions); the two accumulator
@@ -216,8 +224,9 @@ struct Cfg {
   // four regions (192 columns) let the copy warps run up to three steps
   // ahead; the accumulators then share 192 columns (3 slots drained first)
   static constexpr int kSfRegions = kOverlapAcc ? 4 : kStages;
-  static constexpr int kSfBase = kOverlapAcc ? kTmemCols - kSfRegions * kSfStageCols : kAccCols;
-  static constexpr int kAcc1Col = kOverlapAcc ? kSfBase - 256 : 0;
+  static constexpr int kSfBase = kOverlapAcc ? kTmemCols - kSfRegions * kSfStageCols : kAccCols * (GROUPED ? 2 : 1);
+  // grouped pairs of BN = 128: two accumulators side by side
+  static constexpr int kAcc1Col = kOverlapAcc ? kSfBase - 256 : GROUPED ? kAccCols : 0;
   static constexpr int kSharedSlots = kOverlapAcc ? (256 - kAcc1Col + 63) / 64 : 0;   // drained before release
   static constexpr int kTmemAlloc = kCoRes ? 256 : kTmemCols;         // columns this CTA allocates
   static_assert(kAcc1Col % 32 == 0, "accumulator column alignment");
@@ -228,8 +237,8 @@ struct Cfg {
   static_assert(BN % 16 == 0 && BN <= 256, "MMA N");
   static_assert(!kQx || (SWAP && BN <= 32), "in-kernel activation: swapped tiles, M <= 32");
   static_assert(!(kQx && MX), "in-kernel activation: NVFP4 only");
-  static_assert(!GROUPED || (!kQx && (PAIR || (SWAP && BN == 128))), "grouped: CTA pairs or 128-row swapped tiles");
-  static_assert(!PAIR || (!SWAP && BN == 256 && !kQx), "CTA pairs: normal 256 x 256 tiles");
+  static_assert(!GROUPED || (PAIR && !MX && (BN == 256 || BN == 128)), "grouped: NVFP4 CTA pairs");
+  static_assert(!PAIR || (!SWAP && (BN == 256 || GROUPED) && !kQx), "CTA pairs: normal 256 x 256 tiles");
   static constexpr int kMmaM = PAIR ? 2 * kBM : kBM;                 // MMA M (over the pair)
   static constexpr int kGroupTiles = PAIR ? kGroupP / 2 : kGroupP;   // raster group, in tiles of P
   static_assert(kOffAct % 1024 == 0 && kActCodeBytes % 1024 == 0, "activation tiles on swizzle atoms");
@@ -305,85 +314,110 @@ __device__ __forceinline__ bool work_next(const GemmParams& p, WorkIter& w, int&
   return true;
 }
 
-// Work of one CTA of a grouped GEMM, from the table of groups in shared
-// memory.  Swapped: tiles (group, 128 weight rows, 128 activation rows of
-// the group), the last index fastest so that neighbours share the weight,
-// cut into k-steps and shared out over the first min(grid, units) CTAs.
-// CTA pairs: tiles (group, 256 activation rows, 256 weight rows) t = pair,
-// pair + pairs, ..., rastered inside a group as the plain GEMM does.
+// Work of a CTA pair of a grouped GEMM: tiles of 256 weight rows by up to BN
+// activation rows, numbered (group, weight tile, activation tile) with runs
+// of up to group_p activation tiles fastest, so that tiles in flight share
+// weights and activations in L2.  Groups leave tiles of every size, so they
+// are handed out as pairs get free: the grid has one cluster a tile (an upper
+// bound: the host does not know the offsets), and a running pair takes over
+// the clusters that have not started (cluster launch control), one ahead of
+// the tile it loads.  Dealt out in turn instead, 32768 rows in 64 groups left
+// the busiest pair 24 % above the mean; contiguous shares of equal cost are
+// balanced, but spread the pairs over all groups at once and their activations
+// over more than the L2 (325 us against 219).
+// The even CTA's loading thread asks for work and publishes each tile's number
+// (-1: the end) to every role of both CTAs through a ring of kTileSlots words
+// and barriers in either shared memory.  A slot is written again kTileSlots
+// tiles later; by then every role has read it: none can be more than the
+// pipeline's stages (each tile has a K step) and two accumulators behind the
+// loads.
 struct GroupWork {
-  int64_t u, u_end, U, G;
-  int64_t tile;
-  int kt;
-  bool swap;
-  int g, row0, rows, blk;   // current tile: group, first activation row, rows from there to the group's end, scale block
   const GroupTable* tab;
+  int E, tiles_p, group_p;
+  int total;                // tiles
+  int seq;                  // tiles published or read so far
+  int asked;                // requests made (issuer)
+  bool issuer;
+  bool ok;                  // no wait has run out
+  int g, row0, rows, blk;   // current tile: group, first activation row, rows, first scale block
+  uint32_t ring;            // shared-memory addresses: tile numbers, their barriers, the answer, its barrier
+  uint32_t bars, answer, answer_bar;
+  volatile int* abort_flag;
+  unsigned* err;
+  uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ GroupWork group_work_begin(const GroupedGemmParams& p, bool swap, const GroupTable* tab) {
-  GroupWork w;
-  w.kt = p.kt;
-  w.swap = swap;
-  w.tab = tab;
-  w.tile = 0;
-  w.g = w.row0 = w.rows = w.blk = 0;
-  if (swap) {
-    w.U = (int64_t)tab->blk[p.E] * p.tiles_p * p.kt;
-    w.G = w.U < (int64_t)gridDim.x ? w.U : (int64_t)gridDim.x;
-    const bool has = (int64_t)blockIdx.x < w.G;
-    w.u = has ? unit_begin(blockIdx.x, w.U, w.G) : 0;
-    w.u_end = has ? unit_begin(blockIdx.x + 1, w.U, w.G) : 0;
-  } else {
-    w.U = w.G = 0;
-    w.u = blockIdx.x / 2;
-    w.u_end = (int64_t)tab->blk2[p.E] * p.tiles_q;
+__device__ __forceinline__ void group_publish(const GroupWork& w, int tile) {
+  const int slot = w.seq % kTileSlots;
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    st_cluster_u32(map_to_rank(w.ring + 4 * slot, r), (uint32_t)tile);
+    mbar_arrive_cluster(map_to_rank(w.bars + 8 * slot, r));
   }
-  return w;
 }
 
-__device__ __forceinline__ bool work_next(const GroupedGemmParams& p, GroupWork& w, int& tp, int& tq, int& kb, int& ke) {
-  if (w.u >= w.u_end) return false;
-  const GroupTable& t = *w.tab;
-  if (w.swap) {
-    w.tile = w.u / w.kt;
-    const int tile = (int)w.tile;
-    const int g = find_group(t.blk, p.E, tile / p.tiles_p);
-    const int local = tile - t.blk[g] * p.tiles_p;
-    const int cnt = t.blk[g + 1] - t.blk[g];
-    tp = local / cnt;
-    tq = local - tp * cnt;
-    kb = (int)(w.u - w.tile * w.kt);
-    const int64_t rest = w.u_end - w.u;
-    ke = (int)(kb + rest < w.kt ? kb + rest : w.kt);
-    w.u += ke - kb;
-    w.g = g;
-    w.row0 = t.off[g] + tq * 128;
-    w.blk = t.blk[g] + tq;
-    w.rows = min(t.off[g + 1] - w.row0, 128);
+// Tile number of the next tile, -1 at the end (or when a wait ran out).
+__device__ __forceinline__ int group_next_tile(GroupWork& w) {
+  int tile;
+  if (w.issuer) {
+    while (true) {
+      uint32_t first = blockIdx.x;
+      bool more = true;
+      if (w.asked > 0) {
+        if (!mbar_wait(w.answer_bar, (uint32_t)(w.asked - 1) & 1u, w.abort_flag, w.err, w.timeout_ns)) {
+          w.ok = false;
+          return -1;
+        }
+        more = clc_query(w.answer, first);
+        fence_proxy_async_smem();                           // read before the next asynchronous write
+      }
+      if (more) {
+        mbar_arrive_expect_tx(w.answer_bar, 16);
+        clc_try_cancel(w.answer, w.answer_bar);
+        ++w.asked;
+      }
+      tile = more ? (int)(first / 2) : -1;
+      if (tile < w.total) break;                            // the grid is an upper bound: go on to the next
+    }
+    group_publish(w, tile);
   } else {
-    const int tile = (int)w.u;
-    const int g = find_group(t.blk2, p.E, tile / p.tiles_q);
-    const int local = tile - t.blk2[g] * p.tiles_q;
-    const int cnt = t.blk2[g + 1] - t.blk2[g];
-    const int per = p.group_p * p.tiles_q;
-    const int first = local / per * p.group_p;
-    const int gsize = min(cnt - first, p.group_p);
-    const int l2 = local - first * p.tiles_q;
-    tp = first + l2 % gsize;
-    tq = l2 / gsize;
-    kb = 0;
-    ke = w.kt;
-    w.u += gridDim.x / 2;
-    w.g = g;
-    w.row0 = t.off[g] + tp * 256;
-    w.blk = t.blk[g] + tp * 2;
-    w.rows = t.off[g + 1] - w.row0;
+    if (!mbar_wait_cluster(w.bars + 8 * (w.seq % kTileSlots), (uint32_t)(w.seq / kTileSlots) & 1u, w.abort_flag, w.err,
+                           w.timeout_ns)) {
+      w.ok = false;
+      return -1;
+    }
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tile) : "r"(w.ring + 4 * (w.seq % kTileSlots)) : "memory");
   }
+  ++w.seq;
+  return tile;
+}
+
+template <int BN>
+__device__ __forceinline__ bool group_work_next(GroupWork& w, int& tp, int& tq) {
+  const int tile = group_next_tile(w);
+  if (tile < 0) return false;
+  const GroupTable& t = *w.tab;
+  const int g = find_group(t.tiles, w.E, tile / w.tiles_p);
+  const int local = tile - t.tiles[g] * w.tiles_p;
+  const int cnt = t.tiles[g + 1] - t.tiles[g];
+  const int per = w.group_p * w.tiles_p;
+  const int q0 = local / per * w.group_p;
+  const int run = min(cnt - q0, w.group_p);
+  const int l2 = local - q0 * w.tiles_p;
+  tp = l2 / run;
+  tq = q0 + l2 - tp * run;
+  w.g = g;
+  w.row0 = t.off[g] + tq * BN;
+  w.rows = min(t.off[g + 1] - w.row0, BN);
+  w.blk = t.blk[g] + tq * (BN / 128);
   return true;
 }
 
+__device__ __forceinline__ int64_t row0_of(const GroupWork& w) { return w.row0; }
+__device__ __forceinline__ int64_t row0_of(const WorkIter&) { return 0; }
+
 // One tile's operands: first code rows and first 128-row scale blocks of P
-// and Q, and (grouped, swapped) activation rows.
+// and Q, and (grouped) activation rows that this CTA loads.
 struct TileSrc {
   int p0, q0, pb, qb, rows;
 };
@@ -471,11 +505,13 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar_sf + 8 * s, C::kCopyWarps);
     for (int i = 0; i < C::kCopyWarps; ++i) mbar_init(bar_cp_drain + 8 * i, 1);
     for (int j = 0; j < C::kActSteps; ++j) mbar_init(bar_act + 8 * j, 128);
+    if (GROUPED)
+      for (int s = 0; s <= kTileSlots; ++s) mbar_init(sbase + C::kOffClc + 16 + 8 * s, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&p.tmap_p);
     prefetch_tmap(&p.tmap_q);
-    if (!SWAP && p.tma_store) prefetch_tmap(&p.tmap_out);
+    if (!SWAP && !GROUPED && p.tma_store) prefetch_tmap(&p.tmap_out);
     if (PAIR) {
       prefetch_tmap(&p.tmap_sfa);
       prefetch_tmap(&p.tmap_sfb);
@@ -507,11 +543,41 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
   const GroupTable* tab = reinterpret_cast<const GroupTable*>(smem + C::kOffTab);
   if constexpr (GROUPED) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    load_groups<PAIR>(*reinterpret_cast<GroupTable*>(smem + C::kOffTab), p.offsets, p.E, p.M, p.err);
+    load_groups<BN>(*reinterpret_cast<GroupTable*>(smem + C::kOffTab), p.offsets, p.E, p.M, p.err);
   }
-  auto begin_work = [&]() {
-    if constexpr (GROUPED) return group_work_begin(p, SWAP, tab);
-    else return work_begin(p, SWAP, PAIR);
+  auto begin_work = [&](bool issuer = false) {
+    if constexpr (GROUPED) {
+      GroupWork w;
+      w.tab = tab;
+      w.E = p.E;
+      w.tiles_p = p.tiles_p;
+      w.group_p = p.group_p;
+      w.total = tab->tiles[p.E] * p.tiles_p;
+      w.seq = 0;
+      w.issuer = issuer;
+      w.ok = true;
+      w.g = w.row0 = w.rows = w.blk = 0;
+      w.asked = 0;
+      w.answer = sbase + C::kOffClc;
+      w.answer_bar = w.answer + 16;
+      w.bars = w.answer_bar + 8;
+      w.ring = w.bars + 8 * kTileSlots;
+      w.abort_flag = abort_flag;
+      w.err = p.err;
+      w.timeout_ns = p.timeout_ns;
+      return w;
+    } else {
+      return work_begin(p, SWAP, PAIR);
+    }
+  };
+  auto next_work = [&](auto& w, int& tp, int& tq, int& kb, int& ke) {
+    if constexpr (GROUPED) {
+      kb = 0;
+      ke = p.kt;
+      return group_work_next<BN>(w, tp, tq);
+    } else {
+      return work_next(p, w, tp, tq, kb, ke);
+    }
   };
 
   if (warp == 0) {
@@ -528,22 +594,19 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       bool ok = true;
       // p0: this CTA's first row of P (CTA pairs: its 128-row half of the
       // 256-row tile); q0: the tile's first row of Q
-      auto for_steps = [&](auto w, int first, int count, auto&& fn) {
+      auto for_steps = [&](auto&& w0, int first, int count, auto&& fn) {
         int tp, tq, kb, ke, j = 0;
-        while (j < first + count && work_next(p, w, tp, tq, kb, ke)) {
+        // grouped: the walk asks for work as it goes, so there is only one
+        std::conditional_t<GROUPED, GroupWork&, WorkIter> w = w0;
+        while (ok && j < first + count && next_work(w, tp, tq, kb, ke)) {
           TileSrc t;
-          if constexpr (GROUPED && SWAP) {
-            t.p0 = w.g * (int)p.N + tp * kBM;
-            t.pb = w.g * p.w_blocks + tp;
-            t.q0 = w.row0;
+          if constexpr (GROUPED) {
+            // each CTA of the pair loads half of the MMA's columns
+            t.rows = ((w.rows + 31) & ~31) / 2;
+            t.p0 = w.g * (int)p.N + tp * 2 * kBM + (int)prank * kBM;
+            t.pb = w.g * p.w_blocks + tp * 2 + (int)prank;
+            t.q0 = w.row0 + (int)prank * t.rows;
             t.qb = w.blk;
-            t.rows = w.rows;
-          } else if constexpr (GROUPED) {
-            t.p0 = w.row0 + (int)prank * kBM;
-            t.pb = w.blk + (int)prank;
-            t.q0 = w.g * (int)p.N + tq * BN;
-            t.qb = w.g * p.w_blocks + tq * 2;
-            t.rows = 0;
           } else {
             t.p0 = PAIR ? tp * 2 * kBM + (int)prank * kBM : tp * kBM;
             t.pb = t.p0 >> 7;
@@ -555,7 +618,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             if (j >= first) fn(j, t, k);
         }
       };
-      // grouped, swapped: index of the box that holds the tile's rows
+      // grouped: index of the box that holds the rows
       auto box_of = [](int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; };
       auto nsfb_of = [&](const TileSrc& t) {
         int n = 0;
@@ -583,22 +646,24 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
         const int q0 = t.q0;
         const uint32_t fb = bar_full + 8 * stage;
         if constexpr (PAIR) {
-          // this CTA's 128-row half of the weight tile, and the scales of all
-          // 256 rows (both CTAs copy them into their own TMEM)
-          tma_load_2d_pair(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q, k * C::kRowBytes, q0 + (int)prank * kBM,
-                           fb);
+          // this CTA's 128-row half of the weight tile (grouped: its half of
+          // the activation rows), and the scales of all 256 rows (both CTAs
+          // copy them into their own TMEM)
+          if constexpr (GROUPED)
+            tma_load_2d_pair(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q_box[box_of(t.rows)], k * C::kRowBytes, q0,
+                             fb);
+          else
+            tma_load_2d_pair(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q, k * C::kRowBytes,
+                             q0 + (int)prank * kBM, fb);
 #pragma unroll
-          for (int rb = 0; rb < 2; ++rb)
+          for (int rb = 0; rb < C::kSfbBlocks; ++rb)
             tma_load_2d_pair(sbase + C::kOffSfb + stage * C::kSfbBytes + rb * C::kChunks * kSfChunk, &p.tmap_sfb, 0,
                              (t.qb + rb) * kc + C::kChunks * k, fb);
           return;
         }
         const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
         const int nsfb = nsfb_of(t);
-        if constexpr (GROUPED)
-          tma_load_2d(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q_box[box_of(t.rows)], k * C::kRowBytes, q0, fb);
-        else
-          tma_load_2d(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q, k * C::kRowBytes, q0, fb);
+        tma_load_2d(sbase + C::kOffB + stage * C::kBBytes, &p.tmap_q, k * C::kRowBytes, q0, fb);
 #pragma unroll
         for (int rb = 0; rb < C::kSfbBlocks; ++rb)
           if (rb < nsfb) {
@@ -612,81 +677,101 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
         if constexpr (PAIR) {
           // the even CTA's barrier counts both CTAs' bytes (every box moves
           // its full size; rows past the tensor are zero-filled)
+          const uint32_t q_bytes = GROUPED ? (16u << box_of(t.rows)) * C::kRowBytes : C::kBBytes;
           if (leader)
-            mbar_arrive_expect_tx(bar_full + 8 * stage,
-                                  2 * (C::kABytes + C::kBBytes + C::kSfaBytes + C::kSfbBytes));
+            mbar_arrive_expect_tx(bar_full + 8 * stage, 2 * (C::kABytes + q_bytes + C::kSfaBytes + C::kSfbBytes));
           return;
         }
         const int nch = min(C::kChunks, kc - C::kChunks * k);
         const uint32_t sf_bytes = (uint32_t)nch * kSfChunk;
-        const uint32_t b_bytes = GROUPED ? (16u << box_of(t.rows)) * C::kRowBytes : C::kBBytes;
         mbar_arrive_expect_tx(bar_full + 8 * stage,
-                              C::kABytes + b_bytes + sf_bytes * (1 + (C::kQx ? 0 : nsfb_of(t))));
+                              C::kABytes + C::kBBytes + sf_bytes * (1 + (C::kQx ? 0 : nsfb_of(t))));
       };
-      const auto w0 = begin_work();
-      // prologue: the first kStages stages are free
-      int npro = 0;
-      const bool w_static = p.w_static != 0;
-      for_steps(w0, 0, C::kStages, [&](int j, const TileSrc& t, int k) {
-        npro = j + 1;
-        if constexpr (GROUPED) return;            // nothing to do before the wait: it is over
-        const int p0 = t.p0, q0 = t.q0;
-        if (w_static) {
-          // a weight declared read-only cannot be written by the preceding
-          // kernel: load its first stages now
-          expect(j, t, k);
-          if (SWAP) load_p(j, t, k);
-          else load_q(j, t, k);
-          issued_mask |= 1u << j;
-        } else {
-          const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
-          if (SWAP) {
-            tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, p0);
-            const size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
-            if (bounds_ok(off + sf_bytes <= p.sf_p_bytes, p.err)) bulk_prefetch_l2(p.sf_p + off, sf_bytes);
-          } else {
-            tma_prefetch_l2_2d(&p.tmap_q, k * C::kRowBytes, PAIR ? q0 + (int)prank * kBM : q0);
-          }
-        }
-      });
-      if (SWAP && !GROUPED) {
-        // decode tiles stream each weight byte once: bring the rest of this
-        // CTA's weight range into L2 now, so that HBM keeps streaming while
-        // the preceding kernel finishes (a hint: it reads nothing into the CTA)
-        for_steps(w0, C::kStages, 1 << 30, [&](int, const TileSrc& t, int k) {
-          const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
-          tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, t.p0);
-          const size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
-          if (bounds_ok(off + sf_bytes <= p.sf_p_bytes, p.err)) bulk_prefetch_l2(p.sf_p + off, sf_bytes);
-        });
-      }
-      if constexpr (!GROUPED) asm volatile("griddepcontrol.wait;" ::: "memory");
-      for_steps(w0, 0, npro, [&](int j, const TileSrc& t, int k) {
-        if (w_static) {
-          if (SWAP) {
-            if (!C::kQx) load_q(j, t, k);
-          } else {
-            load_p(j, t, k);
-          }
-        } else {
-          expect(j, t, k);
-          load_p(j, t, k);
-          if (!C::kQx) load_q(j, t, k);
-          issued_mask |= 1u << j;
-        }
-      });
-      int stage = npro % C::kStages;
-      uint32_t phase = npro == C::kStages ? 1u : 0u;
-      if (npro == C::kStages) {
-        for_steps(w0, npro, 1 << 30, [&](int j, const TileSrc& t, int k) {
+      if constexpr (GROUPED) {
+        int stage = 0;
+        uint32_t phase = 0;
+        auto w = begin_work(leader);
+        for_steps(w, 0, 1 << 30, [&](int, const TileSrc& t, int k) {
           if (!ok) return;
           if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.err, p.timeout_ns)) { ok = false; return; }
           expect(stage, t, k);
           load_p(stage, t, k);
-          if (!C::kQx) load_q(stage, t, k);
+          load_q(stage, t, k);
+          issued_mask |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         });
+        // a request that is still out writes into this CTA: let it land (only
+        // a walk that gave up on a wait leaves one)
+        if (leader && !w.ok && w.asked > 0) {
+          volatile int never = 0;
+          (void)mbar_wait(w.answer_bar, (uint32_t)(w.asked - 1) & 1u, &never, p.err, p.drain_ns);
+        }
+      } else {
+        const auto w0 = begin_work();
+        // prologue: the first kStages stages are free
+        int npro = 0;
+        const bool w_static = p.w_static != 0;
+        for_steps(w0, 0, C::kStages, [&](int j, const TileSrc& t, int k) {
+          const int p0 = t.p0, q0 = t.q0;
+          if (w_static) {
+            // a weight declared read-only cannot be written by the preceding
+            // kernel: load its first stages now
+            expect(j, t, k);
+            if (SWAP) load_p(j, t, k);
+            else load_q(j, t, k);
+            issued_mask |= 1u << j;
+          } else {
+            const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
+            if (SWAP) {
+              tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, p0);
+              const size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
+              if (bounds_ok(off + sf_bytes <= p.sf_p_bytes, p.err)) bulk_prefetch_l2(p.sf_p + off, sf_bytes);
+            } else {
+              tma_prefetch_l2_2d(&p.tmap_q, k * C::kRowBytes, PAIR ? q0 + (int)prank * kBM : q0);
+            }
+          }
+          npro = j + 1;
+        });
+        if (SWAP) {
+          // decode tiles stream each weight byte once: bring the rest of this
+          // CTA's weight range into L2 now, so that HBM keeps streaming while
+          // the preceding kernel finishes (a hint: it reads nothing into the CTA)
+          for_steps(w0, C::kStages, 1 << 30, [&](int, const TileSrc& t, int k) {
+            const uint32_t sf_bytes = (uint32_t)min(C::kChunks, kc - C::kChunks * k) * kSfChunk;
+            tma_prefetch_l2_2d(&p.tmap_p, k * C::kRowBytes, t.p0);
+            const size_t off = ((size_t)t.pb * kc + C::kChunks * k) * kSfChunk;
+            if (bounds_ok(off + sf_bytes <= p.sf_p_bytes, p.err)) bulk_prefetch_l2(p.sf_p + off, sf_bytes);
+          });
+        }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        for_steps(w0, 0, npro, [&](int j, const TileSrc& t, int k) {
+          if (w_static) {
+            if (SWAP) {
+              if (!C::kQx) load_q(j, t, k);
+            } else {
+              load_p(j, t, k);
+            }
+          } else {
+            expect(j, t, k);
+            load_p(j, t, k);
+            if (!C::kQx) load_q(j, t, k);
+            issued_mask |= 1u << j;
+          }
+        });
+        int stage = npro % C::kStages;
+        uint32_t phase = npro == C::kStages ? 1u : 0u;
+        if (npro == C::kStages) {
+          for_steps(w0, npro, 1 << 30, [&](int j, const TileSrc& t, int k) {
+            if (!ok) return;
+            if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.err, p.timeout_ns)) { ok = false; return; }
+            expect(stage, t, k);
+            load_p(stage, t, k);
+            if (!C::kQx) load_q(stage, t, k);
+            last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+            if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+          });
+        }
       }
       // let every issued copy land before the CTA exits, whichever role may
       // have given up (when nothing did, the last load of each stage has
@@ -718,11 +803,13 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     auto w = begin_work();
     int tp, tq, kb0, ke0;
     // CTA pairs: only the even CTA issues (for both)
-    while (ok && leader && work_next(p, w, tp, tq, kb0, ke0)) {
+    while (ok && leader && next_work(w, tp, tq, kb0, ke0)) {
       if (!mbar_wait(bar_acc_empty, acc_phase ^ 1, abort_flag, p.err, p.timeout_ns)) break;
       tc_fence_after();
       uint32_t idesc = idesc_full;
-      if constexpr (GROUPED && SWAP) idesc = idesc_nvf4(C::kMmaM, (w.rows + 15) & ~15);   // columns this tile has
+      // as many columns as the tile has rows; each CTA of a pair holds half
+      // of them, in whole 8-row groups
+      if constexpr (GROUPED) idesc = idesc_nvf4(C::kMmaM, (w.rows + 31) & ~31);
       const uint32_t acc = tmem_base + (acc_buf ? C::kAcc1Col : 0);
       for (int k = kb0; k < ke0; ++k) {
         if (C::kQx && lstep >= C::kActSteps) {     // the host sizes the grid so this cannot happen
@@ -800,11 +887,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     uint32_t acc_phase = 0, acc_buf = 0;
     uint32_t out_buf = 0;                    // next staging buffer (TMA store path)
     auto w = begin_work();
-    int64_t U = (int64_t)p.tiles_p * p.kt, G = gridDim.x;
-    if constexpr (GROUPED) {
-      U = w.U;
-      G = w.G;
-    }
+    const int64_t U = (int64_t)p.tiles_p * p.kt, G = gridDim.x;
     int tp, tq, kb0, ke0;
     bool first_item = true;
     if constexpr (C::kQx) {
@@ -911,30 +994,138 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
         mbar_arrive(bar_acc_empty);
       }
     };
-    while (work_next(p, w, tp, tq, kb0, ke0)) {
+    while (next_work(w, tp, tq, kb0, ke0)) {
       // CTA pairs: this CTA's rows are its 128-row half of the 256-row tile
-      int64_t p0 = PAIR ? (int64_t)tp * 2 * kBM + (int64_t)prank * kBM : (int64_t)tp * kBM;
-      int64_t q0 = (int64_t)tq * BN;
-      // first row past the tile's group (grouped), and whether this tile's
-      // rows go out through TMA stores, which write all 128 rows of a box
-      int64_t m_end = M;
-      bool tma_tile = tma_store;
+      const int64_t p0 = PAIR ? (int64_t)tp * 2 * kBM + (int64_t)prank * kBM : (int64_t)tp * kBM;
+      const int64_t q0 = GROUPED ? row0_of(w) : (int64_t)tq * BN;
       float g_alpha = 0.0f;
       if constexpr (GROUPED) {
-        if constexpr (SWAP) {
-          q0 = w.row0;
-          m_end = (int64_t)w.row0 + w.rows;
-        } else {
-          p0 = (int64_t)w.row0 + (int64_t)prank * kBM;
-          m_end = (int64_t)w.row0 + w.rows;
-          tma_tile = tma_store && p0 + kBM <= m_end;
-        }
         g_alpha = (float)(1.0 / ((double)__ldg(p.ga + w.g) * (double)__ldg(p.gw + w.g)));
       }
       if (!mbar_wait(bar_acc_full, acc_phase, abort_flag, p.err, p.timeout_ns)) break;
       __syncwarp();
       tc_fence_after();
-      if constexpr (!SWAP) {
+      if constexpr (GROUPED && PAIR) {
+        // Lane = weight row = output column n, accumulator column = activation
+        // row, as in swapped tiles: 64 (FP32 output: 32) rows at a time go
+        // through a 16 KB buffer as [row][128 columns] and out in 16-byte
+        // pieces, masked by the group's end, so no row of a neighbour is
+        // touched.  A buffer is rewritten only after a barrier that follows
+        // its last reads.
+        const uint32_t tacc = taddr + (acc_buf ? C::kAcc1Col : 0);
+        auto slot_col = [&](int slot) -> int {
+          return C::kOverlapAcc && acc_buf == 0 ? ((slot + 4 - C::kSharedSlots) & 3) * 64 : slot * 64;
+        };
+        constexpr int kEsz = OUT_F32 ? 4 : 2;
+        const bool vec = p.tma_store != 0;            // output rows start on 16-byte boundaries
+        auto flush = [&](uint32_t buf, int col) {     // a staged buffer, rows col ... of the tile
+          if (col >= w.rows) return;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int id = et + 128 * j;
+            const int r = id / (8 * kEsz), ch = id % (8 * kEsz);
+            const int64_t n = p0 + ch * (16 / kEsz);
+            if (col + r >= w.rows || n >= N) continue;
+            const int64_t o = (q0 + col + r) * N + n;
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(buf + id * 16)
+                         : "memory");
+            if (vec && n + 16 / kEsz <= N) {
+              if (bounds_ok((uint64_t)(o + 16 / kEsz) <= p.out_elems, p.err))
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.out) + o * kEsz) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16 / kEsz; ++e)
+                if (n + e < N && bounds_ok((uint64_t)(o + e) < p.out_elems, p.err)) {
+                  if constexpr (OUT_F32) reinterpret_cast<uint32_t*>(p.out)[o + e] = v[e];
+                  else reinterpret_cast<uint16_t*>(p.out)[o + e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+                }
+            }
+          }
+        };
+        if constexpr (!OUT_F32) {
+          // slots in drain order: the first two straight into the buffers, the
+          // third into registers, then TMEM goes back and the rest follows
+          const uint32_t buf0 = sbase + C::kOffOut, buf1 = buf0 + kStageOutBytes;
+          auto load_slot = [&](int col, uint32_t (&v)[32]) {
+            if (col >= w.rows) return;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(tacc + col + 32 * h, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                v[h * 16 + i] = pack_bf16x2(__fmul_rn(__uint_as_float(r[2 * i]), g_alpha),
+                                            __fmul_rn(__uint_as_float(r[2 * i + 1]), g_alpha));
+            }
+          };
+          auto stage_slot = [&](int col, uint32_t buf, const uint32_t (&v)[32]) {
+            if (col >= w.rows) return;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2 * i * 256 + row * 2),
+                           "h"((uint16_t)(v[i] & 0xFFFFu))
+                           : "memory");
+              asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + (2 * i + 1) * 256 + row * 2),
+                           "h"((uint16_t)(v[i] >> 16))
+                           : "memory");
+            }
+          };
+          static_assert(C::kSharedSlots == (BN == 256 ? 3 : 0), "slots drained before the accumulator goes back");
+          uint32_t v[32];
+          // two accumulators side by side: the next tile's is free already
+          if (!C::kOverlapAcc) release_acc();
+          named_bar_sync(kEpiBar, 128);               // the last tile's reads of both buffers are done
+          load_slot(slot_col(0), v);
+          stage_slot(slot_col(0), buf0, v);
+          load_slot(slot_col(1), v);
+          stage_slot(slot_col(1), buf1, v);
+          if constexpr (BN == 256) {
+            load_slot(slot_col(2), v);
+            release_acc();
+          }
+          named_bar_sync(kEpiBar, 128);
+          flush(buf0, slot_col(0));
+          flush(buf1, slot_col(1));
+          if constexpr (BN == 256) {
+            named_bar_sync(kEpiBar, 128);
+            stage_slot(slot_col(2), buf0, v);
+            load_slot(slot_col(3), v);
+            stage_slot(slot_col(3), buf1, v);
+            named_bar_sync(kEpiBar, 128);
+            flush(buf0, slot_col(2));
+            flush(buf1, slot_col(3));
+          }
+        } else {
+          if (!C::kOverlapAcc) release_acc();
+#pragma unroll 1
+          for (int cc = 0; cc < BN / 32; ++cc) {
+            const int col = slot_col(cc / 2) + (cc & 1) * 32;
+            const bool has = col < w.rows;
+            uint32_t r[32];
+            __syncwarp();
+            if (has) {
+              tmem_ld_32x32b_x32(tacc + col, r);
+              tmem_ld_wait();
+            }
+            if (C::kOverlapAcc && cc == 2 * C::kSharedSlots - 1) release_acc();
+            if (!has) continue;
+            const uint32_t buf = sbase + C::kOffOut + out_buf * kStageOutBytes;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + i * 512 + row * 4),
+                           "f"(__fmul_rn(__uint_as_float(r[i]), g_alpha))
+                           : "memory");
+            named_bar_sync(kEpiBar, 128);
+            flush(buf, col);
+            out_buf ^= 1;
+          }
+        }
+      } else if constexpr (!SWAP) {
         const int64_t m = p0 + row;
         // 64-column slots are drained starting with the columns this buffer
         // shares with the other one; TMEM is handed back right after them.
@@ -957,12 +1148,12 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             // one scale for the whole 64-column slot unless a segment
             // boundary falls inside it
             int seg_lo = 0, seg_hi = 0;
-            if (!GROUPED && n_seg > 1) {
+            if (n_seg > 1) {
               seg_lo = seg_index_smem(seg_end_s, n_seg, n0);
               seg_hi = seg_index_smem(seg_end_s, n_seg, n0 + 63 < N ? n0 + 63 : N - 1);
             }
-            if (GROUPED || seg_lo == seg_hi) {
-              const float a = GROUPED ? g_alpha : seg_alpha_s[seg_lo];
+            if (seg_lo == seg_hi) {
+              const float a = seg_alpha_s[seg_lo];
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 packed[slot * 32 + i] = pack_bf16x2(__fmul_rn(__uint_as_float(r0[2 * i]), a),
@@ -987,7 +1178,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             }
           }
           if (!C::kOverlapAcc) release_acc();
-          if (tma_tile) {
+          if (tma_store) {
             // 64-column sub-tiles through two 16 KB swizzled staging buffers
 #pragma unroll
             for (int sub = 0; sub < BN / 64; ++sub) {
@@ -1014,20 +1205,11 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
               }
               out_buf ^= 1;
             }
-          } else if (m < m_end) {
+          } else if (m < M) {
             __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.out) + m * N;
 #pragma unroll
             for (int c = 0; c < BN / 8; ++c) {
               const int64_t n = q0 + slot_col(c / 8) + (c % 8) * 8;
-              if constexpr (GROUPED) {
-                // the last rows of a group: 16-byte stores where rows allow them
-                if (tma_store && n + 8 <= N) {
-                  if (bounds_ok((uint64_t)(m * N + n + 8) <= p.out_elems, p.err))
-                    *reinterpret_cast<uint4*>(orow + n) =
-                        make_uint4(packed[4 * c], packed[4 * c + 1], packed[4 * c + 2], packed[4 * c + 3]);
-                  continue;
-                }
-              }
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (n + e < N && bounds_ok((uint64_t)(m * N + n + e) < p.out_elems, p.err))
@@ -1047,12 +1229,12 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             if (cc == 2 * C::kSharedSlots - 1 && C::kOverlapAcc) release_acc();
             const int64_t n0 = q0 + c * 32;
             int seg_lo = 0, seg_hi = 0;
-            if (!GROUPED && n_seg > 1) {
+            if (n_seg > 1) {
               seg_lo = seg_index_smem(seg_end_s, n_seg, n0);
               seg_hi = seg_index_smem(seg_end_s, n_seg, n0 + 31 < N ? n0 + 31 : N - 1);
             }
-            if (GROUPED || seg_lo == seg_hi) {
-              const float a = GROUPED ? g_alpha : seg_alpha_s[seg_lo];
+            if (seg_lo == seg_hi) {
+              const float a = seg_alpha_s[seg_lo];
 #pragma unroll
               for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__fmul_rn(__uint_as_float(r[i]), a));
             } else {
@@ -1061,7 +1243,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
                 r[i] = __float_as_uint(
                     __fmul_rn(__uint_as_float(r[i]), seg_alpha_smem(seg_end_s, seg_alpha_s, n_seg, n0 + i)));
             }
-            if (tma_tile && q0 + c * 32 < N) {
+            if (tma_store && q0 + c * 32 < N) {
               const uint32_t buf = sbase + C::kOffOut + out_buf * kStageOutBytes;
               if (et == 0) bulk_wait_group_read<1>();
               named_bar_sync(kEpiBar, 128);
@@ -1077,18 +1259,11 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
                 bulk_commit_group();
               }
               out_buf ^= 1;
-            } else if (!tma_tile && m < m_end) {
+            } else if (!tma_store && m < M) {
               float* orow = reinterpret_cast<float*>(p.out) + m * N;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
                 const int64_t n = q0 + c * 32 + i;
-                if constexpr (GROUPED) {
-                  if (tma_store && n - (i & 3) + 4 <= N) {
-                    if ((i & 3) == 0 && bounds_ok((uint64_t)(m * N + n + 4) <= p.out_elems, p.err))
-                      *reinterpret_cast<uint4*>(orow + n) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-                    continue;
-                  }
-                }
                 if (n < N && bounds_ok((uint64_t)(m * N + n) < p.out_elems, p.err)) orow[n] = __uint_as_float(r[i]);
               }
             }
@@ -1100,12 +1275,11 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
         // activation row.  The whole accumulator row goes to registers, then
         // TMEM is handed back.
         const int64_t n = p0 + row;
-        const float alpha = GROUPED ? g_alpha : seg_alpha_smem(seg_end_s, seg_alpha_s, n_seg, n);
+        const float alpha = seg_alpha_smem(seg_end_s, seg_alpha_s, n_seg, n);
         constexpr int kCols = BN < 32 ? BN : 32;
         uint32_t r[(BN + 31) / 32][kCols];
 #pragma unroll
         for (int c = 0; c < (BN + 31) / 32; ++c) {
-          if (GROUPED && q0 + c * 32 >= m_end) break;
           if constexpr (BN >= 32) {
             tmem_ld_32x32b_x32(taddr + c * 32, r[c]);
           } else {
@@ -1126,22 +1300,19 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
           if constexpr (OUT_F32) reinterpret_cast<float*>(p.out)[mm * N + n] = v;
           else reinterpret_cast<__nv_bfloat16*>(p.out)[mm * N + n] = __float2bfloat16_rn(v);
         };
-        int64_t tile_u0 = (int64_t)tp * p.kt;
-        if constexpr (GROUPED) tile_u0 = w.tile * p.kt;
+        const int64_t tile_u0 = (int64_t)tp * p.kt;
         const int64_t c_first = cta_of_unit(tile_u0, U, G);
         const int64_t c_last = cta_of_unit(tile_u0 + p.kt - 1, U, G);
         if (c_first == c_last) {
           // the whole K range of this tile ran here
           if (n < N) {
 #pragma unroll
-            for (int c = 0; c < (BN + 31) / 32; ++c) {
-              if (GROUPED && q0 + c * 32 >= m_end) break;
+            for (int c = 0; c < (BN + 31) / 32; ++c)
 #pragma unroll
               for (int i = 0; i < kCols; ++i) {
                 const int64_t mm = q0 + c * 32 + i;
-                if (mm < m_end) store_out(mm, __fmul_rn(__uint_as_float(r[c][i]), alpha));
+                if (mm < M) store_out(mm, __fmul_rn(__uint_as_float(r[c][i]), alpha));
               }
-            }
           }
         } else {
           // split tile.  The CTA that holds the tile's first K steps (its last
@@ -1157,15 +1328,13 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             const int64_t part0 = (2 * (int64_t)blockIdx.x + (first_item ? 0 : 1)) * BN * kBM + row;
             uint64_t* part = p.ws + part0;
 #pragma unroll
-            for (int c = 0; c < (BN + 31) / 32; ++c) {
-              if (GROUPED && q0 + c * 32 >= m_end) break;
+            for (int c = 0; c < (BN + 31) / 32; ++c)
 #pragma unroll
               for (int i = 0; i < kCols; ++i) {
                 const int mm = c * 32 + i;
-                if (q0 + mm < m_end && bounds_ok((uint64_t)(part0 + (int64_t)mm * kBM) < p.ws_words, p.err))
+                if (q0 + mm < M && bounds_ok((uint64_t)(part0 + (int64_t)mm * kBM) < p.ws_words, p.err))
                   st_full_word(part + (int64_t)mm * kBM, r[c][i]);
               }
-            }
           } else {
             float sum[(BN + 31) / 32][kCols];
 #pragma unroll
@@ -1184,14 +1353,13 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
               // one round polls every word of a 32-column chunk at once
 #pragma unroll
               for (int cb = 0; cb < (BN + 31) / 32; ++cb) {
-                if (GROUPED && q0 + cb * 32 >= m_end) break;
                 uint64_t v[kCols];
                 const uint64_t t0 = globaltimer_ns();
                 while (true) {
 #pragma unroll
                   for (int i = 0; i < kCols; ++i) {
                     const int mm = cb * 32 + i;
-                    v[i] = q0 + mm < m_end ? ld_word(src + (int64_t)mm * kBM) : (uint64_t)kFullTag << 32;
+                    v[i] = q0 + mm < M ? ld_word(src + (int64_t)mm * kBM) : (uint64_t)kFullTag << 32;
                   }
                   uint32_t all = p.test_stall ? 0u : 1u;
 #pragma unroll
@@ -1208,20 +1376,18 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
                 for (int i = 0; i < kCols; ++i) {
                   const int mm = cb * 32 + i;
                   sum[cb][i] = __fadd_rn(sum[cb][i], __uint_as_float((uint32_t)v[i]));
-                  if (q0 + mm < m_end) st_word(src + (int64_t)mm * kBM, 0ull);     // empty again
+                  if (q0 + mm < M) st_word(src + (int64_t)mm * kBM, 0ull);     // empty again
                 }
               }
             }
             if (n < N && ok_all) {
 #pragma unroll
-              for (int cb = 0; cb < (BN + 31) / 32; ++cb) {
-                if (GROUPED && q0 + cb * 32 >= m_end) break;
+              for (int cb = 0; cb < (BN + 31) / 32; ++cb)
 #pragma unroll
                 for (int i = 0; i < kCols; ++i) {
                   const int64_t mm = q0 + cb * 32 + i;
-                  if (mm < m_end) store_out(mm, __fmul_rn(sum[cb][i], alpha));
+                  if (mm < M) store_out(mm, __fmul_rn(sum[cb][i], alpha));
                 }
-              }
             }
           }
         }
@@ -1230,7 +1396,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       acc_buf ^= 1;
       first_item = false;
     }
-    if (tma_store && et == 0) bulk_wait_group<0>();   // stores done before the CTA's smem goes away
+    if (!GROUPED && tma_store && et == 0) bulk_wait_group<0>();   // stores done before the CTA's smem goes away
   } else {
     // ------------------------------------------------------------ scale copies
     // warp 6 copies P's scale chunks of each stage into TMEM, warp 7 + rb the
@@ -1250,7 +1416,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       bool ok = true;
       auto w = begin_work();
       int tp, tq, kb0, ke0;
-      while (ok && work_next(p, w, tp, tq, kb0, ke0)) {
+      while (ok && next_work(w, tp, tq, kb0, ke0)) {
         for (int k = kb0; k < ke0; ++k) {
           if (C::kQx && step >= C::kActSteps) { ok = false; break; }
           // in-kernel activation: this step's scales are written by the epilogue warps

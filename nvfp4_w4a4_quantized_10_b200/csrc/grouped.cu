@@ -121,17 +121,29 @@ __global__ void __launch_bounds__(256) grouped_quantize_kernel(const GroupedQuan
 
 namespace {
 
-// Which tiles multiply: swapped tiles (128 weight rows by up to 128
-// activation rows, K split over the CTAs) stream each expert's weight once
-// and waste nothing on groups of a few rows; CTA pairs (256 x 256) reach the
-// tensor cores' rate once groups fill them.  The host knows only the mean
-// rows of a group.
-bool grouped_swap(int64_t T, int64_t E) { return T < 192 * E; }
+// Activation rows of a tile: 128 while groups are small (each CTA then keeps
+// 6 pipeline stages instead of 4 in flight, which is what streams weights),
+// 256 once they fill it.  The host knows only the mean rows of a group.
+bool grouped_small(int64_t T, int64_t E) { return T < 128 * E; }
+
+template <int BN>
+cudaError_t launch_grouped(GroupedGemmParams& p, const uint8_t* a_scales, const uint8_t* w_scales, int64_t a_blocks,
+                           int64_t w_blocks, const DeviceInfo* d, cudaStream_t st, bool f32) {
+  using C = Cfg<BN, false, 0, false, true, true>;
+  if (!make_sf_map(&p.tmap_sfa, w_scales, w_blocks * 128, p.kc, C::kChunks) ||
+      !make_sf_map(&p.tmap_sfb, a_scales, a_blocks * 128, p.kc, C::kChunks))
+    return cudaErrorInvalidValue;
+  // one cluster for each tile there can be; running pairs take over those that have not started
+  const int64_t tiles = (p.M + (BN - 1) * (p.E < p.M ? p.E : p.M)) / BN * p.tiles_p;
+  if (tiles > (1ll << 30) - 1) return cudaErrorInvalidValue;
+  const int grid = (int)tiles * 2;
+  return f32 ? launch<BN, false, true, 0, false, true, true>(p, d, st, grid, 2)
+             : launch<BN, false, false, 0, false, true, true>(p, d, st, grid, 2);
+}
 
 nvfp4_status run_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* ga, const uint8_t* w_codes,
                               const uint8_t* w_scales, const float* gw, const int32_t* offsets, int E, int64_t T,
-                              int64_t N, int64_t K, void* out, bool f32, void* workspace, size_t workspace_bytes,
-                              const DeviceInfo* d, cudaStream_t st) {
+                              int64_t N, int64_t K, void* out, bool f32, const DeviceInfo* d, cudaStream_t st) {
   GroupedGemmParams p;
   std::memset(&p, 0, sizeof(p));
   p.err = d->err_word;
@@ -150,61 +162,25 @@ nvfp4_status run_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, c
   p.out_elems = (uint64_t)T * (uint64_t)N;
   const int64_t a_blocks = grouped_blocks(T, E), w_blocks = (int64_t)E * p.w_blocks;
   const uint64_t a_sf = (uint64_t)a_blocks * p.kc * kSfChunk, w_sf = (uint64_t)w_blocks * p.kc * kSfChunk;
-  const bool swap = grouped_swap(T, E);
-  if (swap) {
-    using Cf = Cfg<128, true, 0, false, false, true>;
-    if (workspace) {
-      if (workspace_bytes < workspace_need(d, 128)) return NVFP4_ERR_INVALID_ARG;
-      p.ws = static_cast<uint64_t*>(workspace);
-      p.ws_words = workspace_bytes / sizeof(uint64_t);
-    } else {
-      Workspace w;
-      const cudaError_t e = get_workspace(d, st, 128, &w);
-      if (e == cudaErrorNotPermitted) return NVFP4_ERR_UNSUPPORTED;
-      if (e == cudaErrorInvalidValue) return NVFP4_ERR_INVALID_ARG;
-      if (e != cudaSuccess) return cuda_status(e);
-      p.ws = w.ws;
-      p.ws_words = w.bytes / sizeof(uint64_t);
-    }
-    p.rows_p = (int)(E * N);
-    p.rows_q = (int)T;
-    p.sf_p = w_scales;
-    p.sf_q = a_scales;
-    p.sf_p_bytes = w_sf;
-    p.sf_q_bytes = a_sf;
-    p.rb_q = (int)a_blocks;
-    p.kt = (int)ceil_div(K, 64 * Cf::kKB);
-    p.tiles_p = p.w_blocks;
-    if (!make_code_map(&p.tmap_p, w_codes, p.rows_p, K, kBM, Cf::kRowBytes)) return NVFP4_ERR_CUDA;
-    for (int i = 0; i < 4; ++i)
-      if (!make_code_map(&p.tmap_q_box[i], a_codes, T, K, 16 << i, Cf::kRowBytes)) return NVFP4_ERR_CUDA;
-    p.tmap_q = p.tmap_q_box[3];
-    const cudaError_t e = f32 ? launch<128, true, true, 0, false, false, true>(p, d, st, d->sm_count)
-                              : launch<128, true, false, 0, false, false, true>(p, d, st, d->sm_count);
-    return cuda_status(e);
-  }
-  using Cf = Cfg<256, false, 0, false, true, true>;
-  p.rows_p = (int)T;
-  p.rows_q = (int)(E * N);
-  p.sf_p = a_scales;
-  p.sf_q = w_scales;
-  p.sf_p_bytes = a_sf;
-  p.sf_q_bytes = w_sf;
-  p.rb_q = (int)w_blocks;
-  p.kt = (int)ceil_div(K, 64 * Cf::kKB);
-  p.tiles_q = (int)ceil_div(N, 256);
-  p.group_p = Cf::kGroupTiles;
-  p.tma_store = (N * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;
-  if (!make_code_map(&p.tmap_p, a_codes, T, K, kBM, Cf::kRowBytes) ||
-      !make_code_map(&p.tmap_q, w_codes, p.rows_q, K, kBM, Cf::kRowBytes) ||
-      !make_sf_map(&p.tmap_sfa, a_scales, a_blocks * 128, p.kc, Cf::kChunks) ||
-      !make_sf_map(&p.tmap_sfb, w_scales, w_blocks * 128, p.kc, Cf::kChunks) ||
-      (p.tma_store && !make_out_map(&p.tmap_out, out, T, N, f32)))
-    return NVFP4_ERR_CUDA;
-  const int grid = d->sm_count / 2 * 2;
-  const cudaError_t e = f32 ? launch<256, false, true, 0, false, true, true>(p, d, st, grid, 2)
-                            : launch<256, false, false, 0, false, true, true>(p, d, st, grid, 2);
-  return cuda_status(e);
+  // the weight is P, 128 rows a CTA; the activations are Q
+  p.rows_p = (int)(E * N);
+  p.rows_q = (int)T;
+  p.sf_p = w_scales;
+  p.sf_q = a_scales;
+  p.sf_p_bytes = w_sf;
+  p.sf_q_bytes = a_sf;
+  p.rb_q = (int)a_blocks;
+  using C = Cfg<256, false, 0, false, true, true>;
+  p.kt = (int)ceil_div(K, 64 * C::kKB);
+  p.tiles_p = (int)ceil_div(N, 256);
+  p.group_p = C::kGroupTiles;
+  p.tma_store = (N * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;      // 16-byte stores reach every row
+  if (!make_code_map(&p.tmap_p, w_codes, p.rows_p, K, kBM, C::kRowBytes)) return NVFP4_ERR_CUDA;
+  for (int i = 0; i < 4; ++i)
+    if (!make_code_map(&p.tmap_q_box[i], a_codes, T, K, 16 << i, C::kRowBytes)) return NVFP4_ERR_CUDA;
+  p.tmap_q = p.tmap_q_box[3];
+  return cuda_status(grouped_small(T, E) ? launch_grouped<128>(p, a_scales, w_scales, a_blocks, w_blocks, d, st, f32)
+                                         : launch_grouped<256>(p, a_scales, w_scales, a_blocks, w_blocks, d, st, f32));
 }
 
 }  // namespace
@@ -265,39 +241,30 @@ nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_a
   return cuda_status(e);
 }
 
-size_t nvfp4_grouped_workspace_bytes(int64_t T, int n_groups) {
-  if (T < 1 || n_groups < 1 || n_groups > NVFP4_MAX_GROUPS || !grouped_swap(T, n_groups)) return 0;
-  const DeviceInfo* d = device_info();
-  return d ? workspace_need(d, 128) : 0;
-}
-
 nvfp4_status nvfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const float* a_global_scales,
                                 const uint8_t* w_codes, const uint8_t* w_scales, const float* w_global_scales,
                                 const int32_t* group_offsets, int n_groups, int64_t T, int64_t N, int64_t K, void* out,
-                                nvfp4_out_dtype out_dtype, void* workspace, size_t workspace_bytes,
-                                nvfp4_stream_t stream) {
+                                nvfp4_out_dtype out_dtype, nvfp4_stream_t stream) {
   if (!a_codes || !a_scales || !a_global_scales || !w_codes || !w_scales || !w_global_scales || !group_offsets || !out)
     return NVFP4_ERR_INVALID_ARG;
   if (T < 1 || N < 1 || K < 32 || K % 32 != 0 || n_groups < 1) return NVFP4_ERR_INVALID_ARG;
   if (out_dtype != NVFP4_OUT_BF16 && out_dtype != NVFP4_OUT_F32) return NVFP4_ERR_INVALID_ARG;
-  if (!workspace && workspace_bytes != 0) return NVFP4_ERR_INVALID_ARG;
   // coordinates of the stacked weight and of its scale chunks, and tile
   // counts, are 32-bit
   const int64_t lim = (1ll << 31) - 65536;
   if (n_groups > NVFP4_MAX_GROUPS || T > lim || N > lim / n_groups || K > lim ||
       (int64_t)n_groups * ceil_div(N, 128) > lim / ceil_div(K, 64) ||
-      grouped_blocks(T, n_groups) > lim / ceil_div(K, 64) || grouped_blocks(T, n_groups) > lim / ceil_div(N, 128))
+      grouped_blocks(T, n_groups) > lim / ceil_div(K, 64) ||
+      (T / 128 + n_groups) * ceil_div(N, 256) > lim / 2)
     return NVFP4_ERR_UNSUPPORTED;
-  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(out) ||
-      !aligned16(workspace))
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(out))
     return NVFP4_ERR_ALIGNMENT;
   if (!aligned4(a_global_scales) || !aligned4(w_global_scales) || !aligned4(group_offsets)) return NVFP4_ERR_ALIGNMENT;
   const DeviceInfo* d = device_info();
   if (!d) return NVFP4_ERR_CUDA;
   if (d->major != 10) return NVFP4_ERR_UNSUPPORTED;
   return run_grouped_gemm(a_codes, a_scales, a_global_scales, w_codes, w_scales, w_global_scales, group_offsets,
-                          n_groups, T, N, K, out, out_dtype == NVFP4_OUT_F32, workspace, workspace_bytes, d,
-                          (cudaStream_t)stream);
+                          n_groups, T, N, K, out, out_dtype == NVFP4_OUT_F32, d, (cudaStream_t)stream);
 }
 
 }  // extern "C"

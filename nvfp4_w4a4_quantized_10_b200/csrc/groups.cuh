@@ -21,8 +21,8 @@ __host__ __device__ inline int64_t grouped_blocks(int64_t T, int64_t E) {
 
 struct GroupTable {
   int off[kMaxGroups + 1];
-  int blk[kMaxGroups + 1];    // scale blocks of 128 rows before each group
-  int blk2[kMaxGroups + 1];   // tiles of 256 rows before each group (CTA-pair tiles; filled if asked for)
+  int blk[kMaxGroups + 1];     // scale blocks of 128 rows before each group
+  int tiles[kMaxGroups + 1];   // GEMM tiles of kTileRows rows before each group (filled if asked for)
 };
 
 // Fill the table in shared memory; called by every thread of the CTA (at
@@ -30,7 +30,7 @@ struct GroupTable {
 // or pass T are a caller's error that only the device can see: the error
 // word is set and the table says that every group is empty, so no row is
 // touched.
-template <bool kPairs = false>
+template <int kTileRows = 0>
 __device__ __forceinline__ void load_groups(GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t T,
                                             unsigned* err) {
   bool bad = false;
@@ -42,15 +42,15 @@ __device__ __forceinline__ void load_groups(GroupTable& t, const int32_t* __rest
   }
   if (__syncthreads_or(bad)) {
     if (threadIdx.x == 0) atomicCAS(err, 0u, kErrBounds);
-    for (int i = threadIdx.x; i <= E; i += blockDim.x) t.off[i] = t.blk[i] = t.blk2[i] = 0;
+    for (int i = threadIdx.x; i <= E; i += blockDim.x) t.off[i] = t.blk[i] = t.tiles[i] = 0;
     __syncthreads();
     return;
   }
-  auto prefix = [&](int* out, int rows) {
+  auto prefix = [&](int* out, auto&& value) {
     int carry = 0;
     for (int base = 0; base < E; base += 32) {
       const int i = base + (int)(threadIdx.x & 31);
-      int v = i < E ? (t.off[i + 1] - t.off[i] + rows - 1) / rows : 0;
+      int v = i < E ? value(t.off[i + 1] - t.off[i]) : 0;
       const int own = v;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -62,8 +62,8 @@ __device__ __forceinline__ void load_groups(GroupTable& t, const int32_t* __rest
     }
     if ((threadIdx.x & 31) == 0) out[E] = carry;
   };
-  if (threadIdx.x < 32) prefix(t.blk, 128);
-  else if (kPairs && threadIdx.x < 64) prefix(t.blk2, 256);
+  if (threadIdx.x < 32) prefix(t.blk, [](int r) { return (r + 127) >> 7; });
+  else if (kTileRows != 0 && threadIdx.x < 64) prefix(t.tiles, [](int r) { return kTileRows ? (r + kTileRows - 1) / (kTileRows ? kTileRows : 1) : 0; });
   __syncthreads();
 }
 

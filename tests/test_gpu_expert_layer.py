@@ -40,8 +40,6 @@ class Layer:
         self.c2, self.s2 = nv.alloc_grouped(T, E, F, dev)
         self.u = torch.empty(T, 2 * F, dtype=torch.bfloat16, device=dev)
         self.d = torch.empty(T, K, dtype=torch.bfloat16, device=dev)
-        n = nv.nvfp4_grouped_workspace_bytes(T, E)
-        self.ws = torch.zeros(n, dtype=torch.uint8, device=dev) if n else None
         self.out_resid = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
         self.out_codes, self.out_scales = nv.alloc_quantized(M, K, dev)
         self.logits = torch.empty(M, E, device=dev)
@@ -52,9 +50,9 @@ class Layer:
         nv.nvfp4_route(self.logits, nv.ROUTE_SOFTMAX_TOPK, **self.r)
         offs = self.r["group_offsets"]
         nv.nvfp4_grouped_quantize(self.h, offs, self.gs1, self.c1, self.s1, row_index=self.r["row_index"])
-        nv.nvfp4_grouped_gemm(self.c1, self.s1, self.gs1, *self.up[:3], offs, self.u, workspace=self.ws)
+        nv.nvfp4_grouped_gemm(self.c1, self.s1, self.gs1, *self.up[:3], offs, self.u)
         nv.nvfp4_grouped_quantize(self.u, offs, self.gs2, self.c2, self.s2, act=nv.ACT_SWIGLU)
-        nv.nvfp4_grouped_gemm(self.c2, self.s2, self.gs2, *self.down[:3], offs, self.d, workspace=self.ws)
+        nv.nvfp4_grouped_gemm(self.c2, self.s2, self.gs2, *self.down[:3], offs, self.d)
         nv.nvfp4_block_norm(self.d, slots=self.r["slots"], slot_weights=self.r["weights"], residual=self.resid,
                             residual_out=self.out_resid, pre_weight=self.w2, codes=self.out_codes,
                             block_scales=self.out_scales, global_scale=100.0)

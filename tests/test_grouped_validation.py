@@ -57,13 +57,13 @@ def test_grouped_quantize_limits_and_alignment():
         assert gquant(**{name: A1}) == nv.ERR_ALIGNMENT
 
 
-def ggemm(a=A16, sa=A16, ga=A4, w=A16, sw=A16, gw=A4, offs=A4, E=4, T=8, N=16, K=64, out=A16, od=0, ws=None, wsb=0):
-    return nv.lib().nvfp4_grouped_gemm(a, sa, ga, w, sw, gw, offs, E, T, N, K, out, od, ws, wsb, None)
+def ggemm(a=A16, sa=A16, ga=A4, w=A16, sw=A16, gw=A4, offs=A4, E=4, T=8, N=16, K=64, out=A16, od=0):
+    return nv.lib().nvfp4_grouped_gemm(a, sa, ga, w, sw, gw, offs, E, T, N, K, out, od, None)
 
 
 @pytest.mark.parametrize("kw", [dict(a=None), dict(sa=None), dict(ga=None), dict(w=None), dict(sw=None), dict(gw=None),
                                 dict(offs=None), dict(out=None), dict(T=0), dict(N=0), dict(K=0), dict(K=48),
-                                dict(E=0), dict(od=2), dict(wsb=16)])
+                                dict(E=0), dict(od=2)])
 def test_grouped_gemm_invalid(kw):
     assert ggemm(**kw) == nv.ERR_INVALID_ARG
 
@@ -71,6 +71,7 @@ def test_grouped_gemm_invalid(kw):
 def test_grouped_gemm_limits_and_alignment():
     assert ggemm(E=513) == nv.ERR_UNSUPPORTED
     assert ggemm(T=1 << 31) == nv.ERR_UNSUPPORTED
+    assert ggemm(T=1 << 30, N=1 << 20, E=1) == nv.ERR_UNSUPPORTED   # more tiles than a grid has
     assert ggemm(K=1 << 31) == nv.ERR_UNSUPPORTED
     assert ggemm(E=512, N=1 << 23) == nv.ERR_UNSUPPORTED            # 512 N >= 2^31
     assert ggemm(T=(1 << 31) - 65536, K=1 << 16) == nv.ERR_UNSUPPORTED   # scale chunks beyond 32 bits
@@ -78,7 +79,6 @@ def test_grouped_gemm_limits_and_alignment():
         assert ggemm(**{name: A4}) == nv.ERR_ALIGNMENT
     for name in ("ga", "gw", "offs"):
         assert ggemm(**{name: A1}) == nv.ERR_ALIGNMENT
-    assert ggemm(ws=A4, wsb=BIG) == nv.ERR_ALIGNMENT
 
 
 def norm(y=A16, dt=0, M=4, K=64, rows=None, slots=None, sw=None, k=0, pw=None, pwid=0, gate=None, kind=0, res=None,
@@ -137,8 +137,6 @@ def test_size_functions_refuse():
     assert nv.nvfp4_grouped_scale_bytes(1, 1, 24) == 0
     assert nv.nvfp4_route_workspace_bytes(0) == 0
     assert nv.nvfp4_route_workspace_bytes(513) == 0
-    assert nv.nvfp4_grouped_workspace_bytes(0, 1) == 0
-    assert nv.nvfp4_grouped_workspace_bytes(1 << 20, 1) == 0        # many rows a group: no K split
 
 
 def test_binding_refuses_host_tensors():
