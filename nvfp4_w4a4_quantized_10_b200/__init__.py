@@ -307,28 +307,52 @@ def nvfp4_mx_gemm(a_codes, a_scales, w_codes, w_scales, M, N, K, out: torch.Tens
                                                K, _ptr(out), _out_dtype(out), _stream(out)))
 
 
-def _typed(name: str, t, dtype, shape=None, device=None):
-    """Pointer of an optional device tensor whose type (and shape, and device) the call relies on."""
+# The expert-layer and block-norm calls are made once a layer in a decoding
+# step of some ten microseconds, so their marshalling is kept short: raw
+# addresses, one look at each tensor, the device switched only if it has to be.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _device_index(t: torch.Tensor) -> int:
+    if not t.is_cuda:
+        raise ValueError("device tensor expected")
+    return t.get_device()
+
+
+def _at(name: str, t, dtype, shape, index: int):
+    """Address of an optional device tensor whose type, shape (None: any) and device the call relies on."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {dtype} expected, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not on {device}")
-    return _ptr(t)
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, not on cuda:{index}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensor expected")
+    return t.data_ptr()
 
 
-def _room(name: str, t, nbytes: int, device=None):
-    """Pointer of an optional device buffer of at least nbytes bytes."""
+def _room(name: str, t, nbytes: int, index: int):
+    """Address of an optional device buffer of at least nbytes bytes."""
     if t is None:
         return None
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, not on {device}")
-    if t.numel() * t.element_size() < nbytes:
-        raise ValueError(f"{name}: {nbytes} bytes needed, got {t.numel() * t.element_size()}")
-    return _ptr(t)
+    if t.nbytes < nbytes:
+        raise ValueError(f"{name}: {nbytes} bytes needed, got {t.nbytes}")
+    return _at(name, t, t.dtype, None, index)
+
+
+def _call(name: str, fn, index: int, *args) -> None:
+    """fn(*args, stream) on device `index` and torch's current stream there."""
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status != OK:
+        raise Nvfp4Error(name, status)
 
 
 def nvfp4_route_workspace_bytes(n_experts: int) -> int:
@@ -340,18 +364,12 @@ def nvfp4_route(logits: torch.Tensor, norm: int, expert_ids: torch.Tensor, weigh
     """logits [M, E] -> expert_ids, weights, slots [M, top_k], row_index
     [M * top_k], group_offsets [E + 1]; workspace: nvfp4_route_workspace_bytes(E) bytes."""
     M, E = logits.shape
-    k, dev = expert_ids.shape[1], logits.device
-    i32 = torch.int32
-    with torch.cuda.device(dev):
-        _check("nvfp4_route",
-               _lib.nvfp4_route(_ptr(logits), _in_dtype(logits), M, E, k, int(norm),
-                                _typed("expert_ids", expert_ids, i32, (M, k), dev),
-                                _typed("weights", weights, torch.float32, (M, k), dev),
-                                _typed("slots", slots, i32, (M, k), dev),
-                                _typed("row_index", row_index, i32, (M * k,), dev),
-                                _typed("group_offsets", group_offsets, i32, (E + 1,), dev),
-                                _room("workspace", workspace, 0, dev), workspace.numel() * workspace.element_size(),
-                                _stream(logits)))
+    k, d, i32 = expert_ids.shape[1], _device_index(logits), torch.int32
+    pairs = (M, k)
+    _call("nvfp4_route", _lib.nvfp4_route, d, _at("logits", logits, logits.dtype, None, d), _in_dtype(logits), M, E, k,
+          norm, _at("expert_ids", expert_ids, i32, pairs, d), _at("weights", weights, torch.float32, pairs, d),
+          _at("slots", slots, i32, pairs, d), _at("row_index", row_index, i32, (M * k,), d),
+          _at("group_offsets", group_offsets, i32, (E + 1,), d), _room("workspace", workspace, 0, d), workspace.nbytes)
 
 
 def nvfp4_grouped_scale_bytes(T: int, n_groups: int, K: int) -> int:
@@ -369,19 +387,16 @@ def nvfp4_grouped_quantize(x: torch.Tensor, group_offsets: torch.Tensor, global_
                            codes: torch.Tensor, block_scales: torch.Tensor, row_index: torch.Tensor | None = None,
                            act: int = ACT_NONE) -> None:
     """Rows of x [M, K] (SwiGLU: [M, 2K]) in group order -> codes [T, K/2] and grouped scales."""
-    T, K = codes.shape[0], 2 * codes.shape[1]
-    E, dev = group_offsets.shape[0] - 1, x.device
+    T, half = codes.shape
+    K, E, d = 2 * half, group_offsets.shape[0] - 1, _device_index(x)
     if x.dim() != 2 or x.shape[1] != (2 * K if act == ACT_SWIGLU else K):
         raise ValueError(f"x: [M, {2 * K if act == ACT_SWIGLU else K}] expected, got {tuple(x.shape)}")
-    with torch.cuda.device(dev):
-        _check("nvfp4_grouped_quantize",
-               _lib.nvfp4_grouped_quantize(_ptr(x), _in_dtype(x), int(act), x.shape[0], K,
-                                           _typed("row_index", row_index, torch.int32, (T,), dev),
-                                           _typed("group_offsets", group_offsets, torch.int32, (E + 1,), dev), E, T,
-                                           _typed("global_scales", global_scales, torch.float32, (E,), dev),
-                                           _typed("codes", codes, torch.uint8, (T, K // 2), dev),
-                                           _room("block_scales", block_scales, nvfp4_grouped_scale_bytes(T, E, K), dev),
-                                           _stream(x)))
+    _call("nvfp4_grouped_quantize", _lib.nvfp4_grouped_quantize, d, _at("x", x, x.dtype, None, d), _in_dtype(x), act,
+          x.shape[0], K, _at("row_index", row_index, torch.int32, (T,), d),
+          _at("group_offsets", group_offsets, torch.int32, (E + 1,), d), E, T,
+          _at("global_scales", global_scales, torch.float32, (E,), d),
+          _at("codes", codes, torch.uint8, None, d),
+          _room("block_scales", block_scales, _lib.nvfp4_grouped_scale_bytes(T, E, K), d))
 
 
 def nvfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_scales: torch.Tensor,
@@ -389,21 +404,16 @@ def nvfp4_grouped_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, a_global_s
                        group_offsets: torch.Tensor, out: torch.Tensor) -> None:
     """a_codes [T, K/2] with grouped scales times w_codes [E, N, K/2] (scales:
     E TCGEN05 buffers) -> out [T, N]."""
-    T, K = a_codes.shape[0], 2 * a_codes.shape[1]
-    E, N = w_codes.shape[0], w_codes.shape[1]
-    dev, f32 = out.device, torch.float32
-    if tuple(out.shape) != (T, N):
-        raise ValueError(f"out: shape {(T, N)} expected, got {tuple(out.shape)}")
-    with torch.cuda.device(dev):
-        _check("nvfp4_grouped_gemm",
-               _lib.nvfp4_grouped_gemm(_typed("a_codes", a_codes, torch.uint8, None, dev),
-                                       _room("a_scales", a_scales, nvfp4_grouped_scale_bytes(T, E, K), dev),
-                                       _typed("a_global_scales", a_global_scales, f32, (E,), dev),
-                                       _typed("w_codes", w_codes, torch.uint8, (E, N, K // 2), dev),
-                                       _room("w_scales", w_scales, E * nvfp4_scale_bytes(N, K), dev),
-                                       _typed("w_global_scales", w_global_scales, f32, (E,), dev),
-                                       _typed("group_offsets", group_offsets, torch.int32, (E + 1,), dev), E, T, N, K,
-                                       _ptr(out), _out_dtype(out), _stream(out)))
+    T, half = a_codes.shape
+    E, N, _ = w_codes.shape
+    K, d, f32, u8 = 2 * half, _device_index(out), torch.float32, torch.uint8
+    _call("nvfp4_grouped_gemm", _lib.nvfp4_grouped_gemm, d, _at("a_codes", a_codes, u8, None, d),
+          _room("a_scales", a_scales, _lib.nvfp4_grouped_scale_bytes(T, E, K), d),
+          _at("a_global_scales", a_global_scales, f32, (E,), d), _at("w_codes", w_codes, u8, (E, N, half), d),
+          _room("w_scales", w_scales, E * _lib.nvfp4_scale_bytes(N, K, SF_TCGEN05), d),
+          _at("w_global_scales", w_global_scales, f32, (E,), d),
+          _at("group_offsets", group_offsets, torch.int32, (E + 1,), d), E, T, N, K,
+          _at("out", out, out.dtype, (T, N), d), _out_dtype(out))
 
 
 def nvfp4_block_norm(y: torch.Tensor, slots: torch.Tensor | None = None, slot_weights: torch.Tensor | None = None,
@@ -415,24 +425,17 @@ def nvfp4_block_norm(y: torch.Tensor, slots: torch.Tensor | None = None, slot_we
                      layout: int = SF_TCGEN05) -> None:
     """y [M, K], or [rows, K] with slots and slot_weights [M, top_k]; post_weight
     of K columns, or of one head; the other rows [M, K] of y's dtype."""
-    K, dev, f32 = y.shape[1], y.device, torch.float32
-    M, k = (y.shape[0], 0) if slots is None else slots.shape
+    rows, K = y.shape
+    d, t, f32 = _device_index(y), y.dtype, torch.float32
+    M, k = (rows, 0) if slots is None else slots.shape
     row = (M, K)
-    with torch.cuda.device(dev):
-        _check("nvfp4_block_norm",
-               _lib.nvfp4_block_norm(_ptr(y), _in_dtype(y), M, K, y.shape[0],
-                                     _typed("slots", slots, torch.int32, (M, k), dev),
-                                     _typed("slot_weights", slot_weights, f32, (M, k), dev), k,
-                                     _typed("post_weight", post_weight, f32, None, dev),
-                                     0 if post_weight is None else post_weight.numel(),
-                                     _typed("gate", gate, y.dtype, row, dev), int(gate_kind),
-                                     _typed("residual", residual, y.dtype, row, dev), float(residual_scale),
-                                     _typed("residual_out", residual_out, y.dtype, row, dev),
-                                     _typed("pre_weight", pre_weight, f32, (K,), dev), float(eps),
-                                     _typed("out", out, y.dtype, row, dev),
-                                     _typed("codes", codes, torch.uint8, (M, K // 2), dev),
-                                     _room("block_scales", block_scales, nvfp4_scale_bytes(M, K, layout), dev),
-                                     float(global_scale), int(layout), _stream(y)))
+    _call("nvfp4_block_norm", _lib.nvfp4_block_norm, d, _at("y", y, t, None, d), _in_dtype(y), M, K, rows,
+          _at("slots", slots, torch.int32, (M, k), d), _at("slot_weights", slot_weights, f32, (M, k), d), k,
+          _at("post_weight", post_weight, f32, None, d), 0 if post_weight is None else post_weight.numel(),
+          _at("gate", gate, t, row, d), gate_kind, _at("residual", residual, t, row, d), residual_scale,
+          _at("residual_out", residual_out, t, row, d), _at("pre_weight", pre_weight, f32, (K,), d), eps,
+          _at("out", out, t, row, d), _at("codes", codes, torch.uint8, (M, K // 2), d),
+          _room("block_scales", block_scales, _lib.nvfp4_scale_bytes(M, K, layout), d), global_scale, layout)
 
 
 def nvfp4_convert_e4m3(x: torch.Tensor, out: torch.Tensor) -> None:
