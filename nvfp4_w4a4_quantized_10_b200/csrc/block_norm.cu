@@ -19,11 +19,15 @@
 #include "common.h"
 #include "ptx.cuh"
 
+#include <initializer_list>
+
 namespace nvfp4 {
 
-constexpr int kNormMaxThreads = 512;
-constexpr int kNormMaxBlocks = 4;                                   // 16-element blocks of a thread
-constexpr int kNormMaxK = kNormMaxThreads * kNormMaxBlocks * 16;    // 32768
+constexpr int kNormMaxK = 32768;
+
+// Most threads of a CTA whose threads own NB 16-element blocks: K up to 8192,
+// 18432 and 32768.
+constexpr int norm_threads(int nb) { return nb == 2 ? 576 : 512; }
 
 struct NormParams {
   const void* y;
@@ -47,58 +51,48 @@ struct NormParams {
   int tc_layout;
   int64_t kc;
   uint64_t codes_bytes, scale_bytes, row_elems;
+  int wide;                // every row and weight starts on a 32-byte boundary
   unsigned* err;
 };
 
-// A block that the same thread may overwrite later (outputs may be the
-// inputs' own buffers): a plain load, not the read-only path.
 template <bool kF32>
-__device__ __forceinline__ void load_block_rw(const void* p, Block16<kF32>& B) {
-  const uint4* q = reinterpret_cast<const uint4*>(p);
-#pragma unroll
-  for (int i = 0; i < (kF32 ? 4 : 2); ++i) B.v[i] = __ldcg(q + i);
-}
-
-template <bool kF32>
-__device__ __forceinline__ void store_block(void* base, int64_t elem, const float (&f)[16]) {
+__device__ __forceinline__ void store_block(void* p, const float (&f)[16], bool wide) {
+  uint4 v[kF32 ? 4 : 2];
   if constexpr (kF32) {
-    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + elem);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+    for (int i = 0; i < 4; ++i)
+      v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                        __float_as_uint(f[4 * i + 3]));
   } else {
     uint32_t w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(base) + elem);
-    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    v[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    v[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+#pragma unroll
+  for (int i = 0; i < (kF32 ? 2 : 1); ++i)
+    st_32b(reinterpret_cast<uint8_t*>(p) + 32 * i, v[2 * i], v[2 * i + 1], wide);
 }
 
-__device__ __forceinline__ void load_weights(const float* w, int at, float (&f)[16]) {
-  const float4* q = reinterpret_cast<const float4*>(w + at);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 v = __ldg(q + i);
-    f[4 * i] = v.x;
-    f[4 * i + 1] = v.y;
-    f[4 * i + 2] = v.z;
-    f[4 * i + 3] = v.w;
-  }
+__device__ __forceinline__ void load_weights(const float* w, int at, float (&f)[16], bool wide) {
+  Block16<true> B;
+  load_block_wide<true>(w + at, B, wide);
+  block_floats<true>(B, f);
 }
 
 // Sum over the threads of one row: a warp, or the whole CTA.  The order is
-// fixed, so results do not depend on timing.
+// fixed, so results do not depend on timing.  red: one slot a warp, another
+// array for each sum of a row, so that one barrier is enough.
 template <bool kWarpRow>
 __device__ __forceinline__ float row_sum(float v, float* red, int warps) {
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
   if constexpr (kWarpRow) return v;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();                       // red may still be read from the last use
   if (lane == 0) red[warp] = v;
   __syncthreads();
   float s = lane < warps ? red[lane] : 0.0f;
@@ -107,11 +101,16 @@ __device__ __forceinline__ float row_sum(float v, float* red, int warps) {
   return s;
 }
 
-// NB: 16-element blocks of a thread; kWarpRow: a warp owns a row (K <= 512 NB),
-// else a CTA does.
-template <bool kF32, int NB, bool kWarpRow>
-__global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormParams p) {
-  __shared__ float red[kNormMaxThreads / 32];
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// NB: 16-element blocks of a thread; kWarpRow: a warp owns a row (K <= 512
+// NB), else a CTA does.  One row and done: the block scheduler then keeps
+// every SM's loads coming while other rows wait in their reductions (16384 x
+// 5120 bf16, residual and norm: 121 us; a persistent grid of 2, 3, 4 or 6 CTAs
+// an SM that walks the rows: 143, 168, 129, 148).
+template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate>
+__global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const NormParams p) {
+  __shared__ float red[2][32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warps = blockDim.x >> 5;
@@ -119,20 +118,51 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
   const int nthr = kWarpRow ? 32 : blockDim.x;
   const int nblk = (int)(p.K / 16);
   constexpr int kB = kF32 ? 64 : 32;                             // bytes of a block
+  constexpr int kLine = 128 / kB;                                // blocks of a 128-byte line
+  // more than one block a thread: gate and residual are fetched into L2 and
+  // read where they are used, instead of being held in registers through the
+  // first norm
+  constexpr bool kHold = NB == 1;
   const float inv_k = 1.0f / (float)p.K;
-  int64_t m = kWarpRow ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
-  const int64_t step = kWarpRow ? (int64_t)gridDim.x * warps : gridDim.x;
-  for (; m < p.M; m += step) {
+  const bool wide = p.wide != 0;
+  const int64_t m = kWarpRow ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
+  auto block_at = [&](const void* base, int64_t row, int j) {
+    return reinterpret_cast<const uint8_t*>(base) + (row * nblk + j) * kB;
+  };
+  if (m < p.M) {
     float f[NB][16];
     // ------------------------------------------------ branch
-    if (p.slots == nullptr) {
+    Block16<kF32> R[kHold ? NB : 1], G[kHold && kGate ? NB : 1];
+    auto load_rest = [&](int b, Block16<kF32>& r, Block16<kF32>& g) {
+      const int j = t + b * nthr;
+      r = Block16<kF32>{};
+      if (j < nblk && p.residual) load_block_wide<kF32>(block_at(p.residual, m, j), r, wide);
+      if constexpr (kGate) {
+        g = Block16<kF32>{};
+        if (j < nblk) load_block_wide<kF32>(block_at(p.gate, m, j), g, wide);
+      }
+    };
+    if constexpr (kHold) {
+      load_rest(0, R[0], G[0]);
+    } else {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int j = t + b * nthr;
-        Block16<kF32> B = {};
-        if (j < nblk) load_block_rw<kF32>(reinterpret_cast<const uint8_t*>(p.y) + (m * nblk + j) * kB, B);
-        block_floats<kF32>(B, f[b]);
+        if (j >= nblk || j % kLine != 0) continue;
+        if (p.residual) prefetch_l2(block_at(p.residual, m, j));
+        if (kGate) prefetch_l2(block_at(p.gate, m, j));
       }
+    }
+    if constexpr (!kSlots) {
+      Block16<kF32> B[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int j = t + b * nthr;
+        B[b] = Block16<kF32>{};
+        if (j < nblk) load_block_wide<kF32>(block_at(p.y, m, j), B[b], wide);
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) block_floats<kF32>(B[b], f[b]);
     } else {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -161,7 +191,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
             const int j = t + b * nthr;
             B[c][b] = Block16<kF32>{};
             if (src[c] >= 0 && j < nblk)                         // -1: a slot the router left empty
-              load_block_at<kF32>(reinterpret_cast<const uint8_t*>(p.y) + (src[c] * nblk + j) * kB, B[c][b]);
+              load_block_wide<kF32>(block_at(p.y, src[c], j), B[c][b], wide);
           }
         }
 #pragma unroll
@@ -177,18 +207,6 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
         }
       }
     }
-    // the row's other inputs are in flight while the branch is normed
-    Block16<kF32> R[NB], G[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int j = t + b * nthr;
-      R[b] = Block16<kF32>{};
-      G[b] = Block16<kF32>{};
-      if (j < nblk) {
-        if (p.residual) load_block_rw<kF32>(reinterpret_cast<const uint8_t*>(p.residual) + (m * nblk + j) * kB, R[b]);
-        if (p.gate) load_block_rw<kF32>(reinterpret_cast<const uint8_t*>(p.gate) + (m * nblk + j) * kB, G[b]);
-      }
-    }
     // ------------------------------------------------ norm after the block
     if (p.post_weight) {
       float ss[NB];
@@ -202,7 +220,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
         float s = 0.0f;
 #pragma unroll
         for (int b = 0; b < NB; ++b) s += ss[b];
-        s = row_sum<kWarpRow>(s, red, warps);
+        s = row_sum<kWarpRow>(s, red[0], warps);
 #pragma unroll
         for (int b = 0; b < NB; ++b) ss[b] = s;
       } else {
@@ -219,7 +237,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
         if (j >= nblk) continue;
         const float r = rsqrtf(fmaf(ss[b], inv, p.eps));
         float w[16];
-        load_weights(p.post_weight, p.post_width == (int)p.K ? j * 16 : (j * 16) & (p.post_width - 1), w);
+        load_weights(p.post_weight, p.post_width == (int)p.K ? j * 16 : (j * 16) & (p.post_width - 1), w, wide);
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[b][i] = f[b][i] * r * w[i];
       }
@@ -230,8 +248,15 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
     for (int b = 0; b < NB; ++b) {
       const int j = t + b * nthr;
       float x[16];
-      if (p.gate_kind != NVFP4_GATE_NONE) {
-        block_floats<kF32>(G[b], x);
+      Block16<kF32> rb, gb;
+      if constexpr (kHold) {
+        rb = R[b];
+        if constexpr (kGate) gb = G[b];
+      } else {
+        load_rest(b, rb, gb);
+      }
+      if constexpr (kGate) {
+        block_floats<kF32>(gb, x);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           float a = x[i];
@@ -242,25 +267,25 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
           f[b][i] *= a;
         }
       }
-      block_floats<kF32>(R[b], x);
+      block_floats<kF32>(rb, x);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         f[b][i] = fmaf(p.residual_scale, f[b][i], x[i]);
         s = fmaf(f[b][i], f[b][i], s);
       }
       if (p.residual_out && j < nblk && bounds_ok((uint64_t)((m * nblk + j + 1) * 16) <= p.row_elems, p.err))
-        store_block<kF32>(p.residual_out, (m * nblk + j) * 16, f[b]);
+        store_block<kF32>(const_cast<uint8_t*>(block_at(p.residual_out, m, j)), f[b], wide);
     }
     // ------------------------------------------------ norm before the next block
     if (p.pre_weight) {
-      s = row_sum<kWarpRow>(s, red, warps);
+      s = row_sum<kWarpRow>(s, red[1], warps);
       const float r = rsqrtf(fmaf(s, inv_k, p.eps));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int j = t + b * nthr;
         if (j >= nblk) continue;
         float w[16];
-        load_weights(p.pre_weight, j * 16, w);
+        load_weights(p.pre_weight, j * 16, w, wide);
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[b][i] = f[b][i] * r * w[i];
       }
@@ -271,7 +296,7 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
       const int j = t + b * nthr;
       if (j >= nblk) continue;
       if (p.out && bounds_ok((uint64_t)((m * nblk + j + 1) * 16) <= p.row_elems, p.err))
-        store_block<kF32>(p.out, (m * nblk + j) * 16, f[b]);
+        store_block<kF32>(const_cast<uint8_t*>(block_at(p.out, m, j)), f[b], wide);
       if (p.codes) {
         float amax = 0.0f;
 #pragma unroll
@@ -307,23 +332,29 @@ __global__ void __launch_bounds__(kNormMaxThreads) block_norm_kernel(const NormP
 
 namespace {
 
+template <bool kF32, int NB, bool kWarpRow>
+cudaError_t launch_norm_as(const NormParams& p, int grid, int threads, cudaStream_t st) {
+  if (p.slots)
+    return p.gate ? launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, true, true>, grid, threads, st, p)
+                  : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, true, false>, grid, threads, st, p);
+  return p.gate ? launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, true>, grid, threads, st, p)
+                : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, false>, grid, threads, st, p);
+}
+
 template <bool kF32>
-cudaError_t launch_norm(const NormParams& p, const DeviceInfo* d, cudaStream_t st) {
+cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
   const int nblk = (int)(p.K / 16);
   // rows of at most 1024: a warp each, 8 to a CTA; longer ones a CTA each
   if (nblk <= 64) {
-    const int64_t want = ceil_div(p.M, 8), cap = (int64_t)d->sm_count * 8;
-    const int grid = (int)(want < cap ? want : cap);
-    return nblk <= 32 ? launch_pdl(block_norm_kernel<kF32, 1, true>, grid, 256, st, p)
-                      : launch_pdl(block_norm_kernel<kF32, 2, true>, grid, 256, st, p);
+    const int grid = (int)ceil_div(p.M, 8);
+    return nblk <= 32 ? launch_norm_as<kF32, 1, true>(p, grid, 256, st) : launch_norm_as<kF32, 2, true>(p, grid, 256, st);
   }
-  const int nb = (int)ceil_div(nblk, kNormMaxThreads);
+  const int nb = nblk <= norm_threads(1) ? 1 : nblk <= 2 * norm_threads(2) ? 2 : 4;
   const int threads = (int)ceil_div(ceil_div(nblk, nb), 32) * 32;
-  const int64_t cap = (int64_t)d->sm_count * (2048 / threads);
-  const int grid = (int)(p.M < cap ? p.M : cap);
-  if (nb == 1) return launch_pdl(block_norm_kernel<kF32, 1, false>, grid, threads, st, p);
-  if (nb == 2) return launch_pdl(block_norm_kernel<kF32, 2, false>, grid, threads, st, p);
-  return launch_pdl(block_norm_kernel<kF32, 4, false>, grid, threads, st, p);
+  const int grid = (int)p.M;
+  if (nb == 1) return launch_norm_as<kF32, 1, false>(p, grid, threads, st);
+  if (nb == 2) return launch_norm_as<kF32, 2, false>(p, grid, threads, st);
+  return launch_norm_as<kF32, 4, false>(p, grid, threads, st);
 }
 
 }  // namespace
@@ -390,9 +421,13 @@ nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, in
   p.codes_bytes = (uint64_t)M * (uint64_t)(K / 2);
   p.scale_bytes = codes ? nvfp4_scale_bytes(M, K, layout) : 0;
   p.row_elems = (uint64_t)M * (uint64_t)K;
+  p.wide = 1;
+  for (const void* q : {y, (const void*)post_weight, gate, residual, (const void*)residual_out,
+                        (const void*)pre_weight, (const void*)out})
+    if (reinterpret_cast<uintptr_t>(q) & 31) p.wide = 0;
   p.err = d->err_word;
   cudaStream_t st = (cudaStream_t)stream;
-  return cuda_status(dtype == NVFP4_IN_F32 ? launch_norm<true>(p, d, st) : launch_norm<false>(p, d, st));
+  return cuda_status(dtype == NVFP4_IN_F32 ? launch_norm<true>(p, st) : launch_norm<false>(p, st));
 }
 
 }  // extern "C"

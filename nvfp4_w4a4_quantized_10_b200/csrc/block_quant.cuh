@@ -101,6 +101,39 @@ __device__ __forceinline__ void load_block_at(const void* p, Block16<kF32>& B) {
   for (int i = 0; i < (kF32 ? 4 : 2); ++i) B.v[i] = __ldg(q + i);
 }
 
+// The same through 32-byte loads and stores, one whole DRAM sector a lane
+// (16-byte ones at this stride use half of each sector they touch, twice).
+// `wide`: the address is 32-byte aligned; else 16-byte pieces.
+__device__ __forceinline__ void ld_32b(const void* p, uint4& a, uint4& b, bool wide) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p)
+                 : "memory");
+  } else {
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *(reinterpret_cast<const uint4*>(p) + 1);
+  }
+}
+
+__device__ __forceinline__ void st_32b(void* p, const uint4& a, const uint4& b, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+                 "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(p) = a;
+    *(reinterpret_cast<uint4*>(p) + 1) = b;
+  }
+}
+
+template <bool kF32>
+__device__ __forceinline__ void load_block_wide(const void* p, Block16<kF32>& B, bool wide) {
+#pragma unroll
+  for (int i = 0; i < (kF32 ? 2 : 1); ++i)
+    ld_32b(reinterpret_cast<const uint8_t*>(p) + 32 * i, B.v[2 * i], B.v[2 * i + 1], wide);
+}
+
 template <bool kF32>
 __device__ __forceinline__ void load_block(const void* x, uint32_t b, Block16<kF32>& B) {
   const uint4* p = reinterpret_cast<const uint4*>(x) + (size_t)b * (kF32 ? 4 : 2);

@@ -33,6 +33,7 @@ struct GroupedQuantParams {
   uint8_t* scales;
   int64_t kc;
   uint64_t codes_bytes, scale_bytes;
+  int wide;                   // rows start on 32-byte boundaries
   unsigned* err;
 };
 
@@ -69,8 +70,8 @@ __global__ void __launch_bounds__(256) grouped_quantize_kernel(const GroupedQuan
       if constexpr (kGlu) C[u] = Block16<kF32>{};
       if (src >= 0 && src < p.M) {
         const uint8_t* q = reinterpret_cast<const uint8_t*>(p.x) + (src * src_stride + j) * (kF32 ? 64 : 32);
-        load_block_at<kF32>(q, B[u]);
-        if constexpr (kGlu) load_block_at<kF32>(q + (int64_t)p.nblk * (kF32 ? 64 : 32), C[u]);
+        load_block_wide<kF32>(q, B[u], p.wide != 0);
+        if constexpr (kGlu) load_block_wide<kF32>(q + (int64_t)p.nblk * (kF32 ? 64 : 32), C[u], p.wide != 0);
       } else {
         atomicCAS(p.err, 0u, kErrBounds);       // a row that x does not have: quantized as zeros
       }
@@ -227,6 +228,7 @@ nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_a
   p.kc = ceil_div(K, 64);
   p.codes_bytes = (uint64_t)T * (uint64_t)(K / 2);
   p.scale_bytes = nvfp4_grouped_scale_bytes(T, n_groups, K);
+  p.wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
   p.err = d->err_word;
   const int64_t want = ceil_div(T * (K / 16), 256);
   const int64_t cap = (int64_t)d->sm_count * 8;

@@ -30,7 +30,7 @@
 
 namespace nvfp4 {
 
-constexpr int kRouteThreads = 512;
+constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kSub = 128;               // tokens ranked at a time
 constexpr int kMaxTopK = NVFP4_MAX_TOP_K;
@@ -110,14 +110,22 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
     const int n = (int)(m_end - sub < kSub ? m_end - sub : kSub);
     for (int i = threadIdx.x; i < E * (kSub / 32); i += kRouteThreads) (&mask[0][0])[i] = 0;
     __syncthreads();
+    // the next token's logits are on their way while this one is selected
+    float x[NV];
+    auto load_token = [&](int ml) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        x[i] = ml < n && e < E ? load_logit<kF32>(p.logits, (sub + ml) * E + e) : -INFINITY;
+      }
+    };
+    load_token(warp);
     for (int ml = warp; ml < n; ml += kRouteWarps) {
       const int64_t m = sub + ml;
       uint32_t key[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        key[i] = e < E ? order_key(load_logit<kF32>(p.logits, m * E + e)) : 0u;
-      }
+      for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
+      load_token(ml + kRouteWarps);
       // softmax over all experts: the sum before any is taken out
       uint32_t best = 0;
 #pragma unroll
@@ -221,6 +229,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int E = p.E, k = p.k;
+  const int64_t m_begin = (int64_t)blockIdx.x * p.chunk;
+  const int64_t m_end = m_begin + p.chunk < p.M ? m_begin + p.chunk : p.M;
+  const int i_end = (int)(m_end * k);
+  int i = (int)(m_begin * k) + threadIdx.x;
+  // the first pair of this thread is on its way while the counts are added up
+  int id = -1, rank = 0;
+  if (i < i_end) {
+    id = __ldg(p.ids + i);
+    rank = p.slots[i];
+  }
   const int e = threadIdx.x & (ep - 1), q = threadIdx.x / ep, parts = kRouteThreads / ep;
   int all = 0, before = 0;
   if (e < E) {
@@ -249,24 +267,25 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[E] = total;
   __syncthreads();
-  const int64_t m_begin = (int64_t)blockIdx.x * p.chunk;
-  const int64_t m_end = m_begin + p.chunk < p.M ? m_begin + p.chunk : p.M;
-  const int i_end = (int)(m_end * k);
-  for (int i = (int)(m_begin * k) + threadIdx.x; i < i_end; i += kRouteThreads) {
-    const int id = __ldg(p.ids + i);
+  while (i < i_end) {
     if (id >= 0) {
-      const int s = base[id] + p.slots[i];
-      p.slots[i] = s;
-      p.row_index[s] = i / k;
+      const int at = base[id] + rank;
+      p.slots[i] = at;
+      p.row_index[at] = i / k;
     }
     if (i >= total) p.row_index[i] = -1;         // rows no pair fills
+    i += kRouteThreads;
+    if (i < i_end) {
+      id = __ldg(p.ids + i);
+      rank = p.slots[i];
+    }
   }
 }
 
 namespace {
 
-// Runs of tokens: one CTA up to 64 tokens (4 a warp: one launch), else at
-// least 16 tokens a run, one for each warp, and at most one run an SM.
+// Runs of tokens: one CTA up to 64 tokens (2 a warp: one launch), else at
+// least 32 tokens a run, one for each warp, and at most one run an SM.
 int64_t route_chunks(int64_t M, int sms) {
   if (M <= 64) return 1;
   const int64_t cap = sms < kRouteMaxChunks ? sms : kRouteMaxChunks;
