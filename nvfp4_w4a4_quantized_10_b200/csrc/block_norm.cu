@@ -111,8 +111,13 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate>
 __global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const NormParams p) {
   __shared__ float red[2][32];
+  __shared__ float quot[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (p.codes) {                         // (uniform) seen by all after this barrier
+    if (threadIdx.x < 8) quot[threadIdx.x] = scale_quotient(p.gs, threadIdx.x);
+    __syncthreads();
+  }
   const int warps = blockDim.x >> 5;
   const int t = kWarpRow ? threadIdx.x & 31 : threadIdx.x;       // thread of the row
   const int nthr = kWarpRow ? 32 : blockDim.x;
@@ -261,8 +266,7 @@ __global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const Norm
         for (int i = 0; i < 16; ++i) {
           float a = x[i];
           if (p.gate_kind != NVFP4_GATE_LINEAR) {
-            a = __frcp_rn(1.0f + expf(-x[i]));
-            if (p.gate_kind == NVFP4_GATE_SILU) a *= x[i];
+            a = p.gate_kind == NVFP4_GATE_SILU ? silu(x[i]) : sigmoid(x[i]);
           }
           f[b][i] *= a;
         }
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const Norm
 #pragma unroll
         for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[b][i]));
         uint32_t lo, hi;
-        const uint32_t sc = quantize_values(f[b], amax, p.gs, lo, hi);
+        const uint32_t sc = quantize_values(f[b], amax, p.gs, quot, lo, hi);
         const int64_t at = m * nblk + j;
         if (bounds_ok((uint64_t)(at + 1) * 8 <= p.codes_bytes, p.err))
           reinterpret_cast<uint2*>(p.codes)[at] = make_uint2(lo, hi);

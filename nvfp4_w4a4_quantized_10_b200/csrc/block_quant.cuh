@@ -231,23 +231,66 @@ __device__ __forceinline__ uint32_t quantize_block(const Block16<kF32>& B, float
   return s;
 }
 
-// The same block from FP32 values with a global scale of its own (groups and
-// fused producers): amax must be the largest magnitude of f.  Bit for bit
-// what quantize_block writes for the same values and scale.
-__device__ __forceinline__ uint32_t quantize_values(const float (&f)[16], float amax, float g, uint32_t& lo,
-                                                    uint32_t& hi) {
-  const float t = __fmul_rn(__fdiv_rn(amax, 6.0f), g);
-  const uint32_t s = cvt_e4m3(t);
-  const float r = recip_entry(g, s);       // 0 for s = 0: codes are signed zeros
+// The same block from FP32 values, for kernels that quantize what they just
+// computed or use one global scale a group: amax must be the largest
+// magnitude of f.  Bit for bit what quantize_block writes for the same values
+// and scale, with the two divisions replaced:
+//   amax / 6   by a product with 1/6 and one fused correction (division by a
+//              constant; Brisebarre, Muller and Raina, "Accelerating correctly
+//              rounded floating-point division when the divisor is known in
+//              advance", 2004), checked against the division for every
+//              mantissa; below 2^-100, where the correction could underflow,
+//              it stays a division;
+//   g / s      by q[m] 2^-e for s = (1 + m/8) 2^e, with the eight quotients
+//              q[m] = g / (1 + m/8) taken once per scale: a power of two
+//              scales a rounded quotient exactly while nothing is subnormal
+//              (g >= 2^-100).
+constexpr float kTinyAmax = 7.888609052210118e-31f;   // 2^-100
+
+// Quotient m of a global scale's table of eight.
+__device__ __forceinline__ float scale_quotient(float g, int m) { return __fdiv_rn(g, 1.0f + (float)m * 0.125f); }
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t quantize_values(const float (&f)[16], float amax, float g, const float* quot,
+                                                    uint32_t& lo, uint32_t& hi) {
+  constexpr float kSixth = 1.0f / 6.0f;
+  const float q0 = __fmul_rn(amax, kSixth);
+  float q = __fmaf_rn(__fmaf_rn(-6.0f, q0, amax), kSixth, q0);
+  if (amax < kTinyAmax) q = __fdiv_rn(amax, 6.0f);
+  const uint32_t s = cvt_e4m3(__fmul_rn(q, g));
+  const uint32_t bits = __float_as_uint(e4m3_to_f32(s));
+  float r = __fmul_rn(quot[(bits >> 20) & 7], __uint_as_float((254u << 23) - (bits & 0x7F800000u)));
+  if (g < kTinyAmax) r = __fdiv_rn(g, __uint_as_float(bits));
+  if (s == 0) r = 0.0f;                    // codes are signed zeros
+  const float2 r2 = make_float2(r, r);
   float y0[8], y1[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    y0[i] = __fmul_rn(f[i], r);
-    y1[i] = __fmul_rn(f[8 + i], r);
+  for (int i = 0; i < 4; ++i) {
+    const float2 u = mul2(make_float2(f[2 * i], f[2 * i + 1]), r2);
+    const float2 v = mul2(make_float2(f[8 + 2 * i], f[9 + 2 * i]), r2);
+    y0[2 * i] = u.x;
+    y0[2 * i + 1] = u.y;
+    y1[2 * i] = v.x;
+    y1[2 * i + 1] = v.y;
   }
   lo = cvt_e2m1x8(y0);
   hi = cvt_e2m1x8(y1);
   return s;
 }
+
+// f * sigmoid(f) and sigmoid(f): exp to 2 ulp, one approximate quotient (2
+// ulp; its flush to zero beyond 2^126 is the limit's own value).
+__device__ __forceinline__ float silu(float f) { return __fdividef(f, 1.0f + expf(-f)); }
+__device__ __forceinline__ float sigmoid(float f) { return __fdividef(1.0f, 1.0f + expf(-f)); }
 
 }  // namespace nvfp4

@@ -17,6 +17,9 @@
 #include "groups.cuh"
 #include "ptx.cuh"
 
+#ifndef QCTAS
+#define QCTAS 6
+#endif
 namespace nvfp4 {
 
 struct GroupedQuantParams {
@@ -26,96 +29,114 @@ struct GroupedQuantParams {
   const int32_t* offsets;
   int E;
   int64_t T;
-  uint32_t nblk;              // K / 16
-  DivU32 div_nblk;
+  int nblk;                   // K / 16
+  int seg;                    // warp-wide runs of 32 blocks in one work item
+  int parts;                  // work items of a row
+  DivU32 div_parts;
   const float* gs;
   uint8_t* codes;
   uint8_t* scales;
-  int64_t kc;
+  uint32_t kc;
   uint64_t codes_bytes, scale_bytes;
   int wide;                   // rows start on 32-byte boundaries
   unsigned* err;
 };
 
-// One thread owns one 16-element block, as in the plain quantizer; a CTA owns
-// a contiguous share of the blocks of all rows that the offsets name, so that
-// it builds the group table once and a thread's group only moves forward.
-// Memory-bound: each source row is read once from HBM (repeats of a gathered
-// row hit L2) and 9/16 byte an element written.
+// One thread owns one 16-element block, as in the plain quantizer; a warp
+// owns a row, or a part of one when rows are few, and walks it 32 blocks at a
+// time, so that the group, the source row and the scale's place are found
+// once an item and every address inside is an immediate offset.  A CTA owns a
+// contiguous share of all items that the offsets name: it builds the table of
+// groups, and the scale quotients of the groups it meets, once.
+// Bound: HBM writes 9/16 byte an element and reads each source row once, but a
+// row gathered k times is read k - 1 times from L2 and encoded k times, and
+// the encoding (some 100 instructions a block) is what it waits for: 2048 rows
+// of 5120 gathered 8 times took 42 us with a flat loop over blocks (214
+// instructions each).
 template <bool kF32, bool kGlu>
 __global__ void __launch_bounds__(256) grouped_quantize_kernel(const GroupedQuantParams p) {
   __shared__ GroupTable tab;
-  constexpr int U = 2;
+  __shared__ float quot[kMaxGroups][8];
+  constexpr int U = kF32 || kGlu ? 2 : 4;                 // loads in flight
+  constexpr int kB = kF32 ? 64 : 32;                      // bytes of a block
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   load_groups(tab, p.offsets, p.E, p.T, p.err);
-  const uint64_t total = (uint64_t)tab.off[p.E] * p.nblk;
-  const uint32_t b_begin = (uint32_t)(total * blockIdx.x / gridDim.x);
-  const uint32_t b_end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
-  if (b_begin >= b_end) return;
-  const int64_t src_stride = (int64_t)p.nblk * (kGlu ? 2 : 1);      // source row, in blocks
-  int g = find_group(tab.off, p.E, (int)div_u32(b_begin, p.div_nblk));
-  float gs = __ldg(p.gs + g);
-  for (uint32_t base = b_begin + threadIdx.x; base < b_end; base += U * 256) {
-    Block16<kF32> B[U], C[kGlu ? U : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint64_t total = (uint64_t)tab.off[p.E] * p.parts;
+  const uint32_t c_begin = (uint32_t)(total * blockIdx.x / gridDim.x);
+  const uint32_t c_end = (uint32_t)(total * (blockIdx.x + 1) / gridDim.x);
+  if (c_begin >= c_end) return;
+  const int g_first = find_group(tab.off, p.E, (int)div_u32(c_begin, p.div_parts));
+  const int g_last = find_group(tab.off, p.E, (int)div_u32(c_end - 1, p.div_parts));
+  for (int i = threadIdx.x; i < (g_last - g_first + 1) * 8; i += 256)
+    quot[i >> 3][i & 7] = scale_quotient(__ldg(p.gs + g_first + (i >> 3)), i & 7);
+  __syncthreads();
+  const uint32_t n = c_end - c_begin;
+  const uint32_t begin = c_begin + n * warp / 8, end = c_begin + n * (warp + 1) / 8;
+  if (begin >= end) return;
+  int g = find_group(tab.off, p.E, (int)div_u32(begin, p.div_parts));
+  const int64_t src_bytes = (int64_t)p.nblk * kB * (kGlu ? 2 : 1);
+  const bool wide = p.wide != 0;
+  const uint32_t lane_scale = (uint32_t)(lane >> 2) * 512 + (lane & 3);
+  for (uint32_t item = begin; item < end; ++item) {
+    const uint32_t row = div_u32(item, p.div_parts);
+    const int j0 = (int)(item - row * p.parts) * p.seg * 32 + lane;
+    const int j_end = min(p.nblk, j0 - lane + p.seg * 32);
+    while ((int)row >= tab.off[g + 1]) ++g;
+    const float gs = __ldg(p.gs + g);
+    const float* q = quot[g - g_first];
+    int64_t src = row;
+    if (p.row_index) src = __ldg(p.row_index + row);
+    const bool have = src >= 0 && src < p.M;
+    if (!have && lane == 0) atomicCAS(p.err, 0u, kErrBounds);   // a row that x does not have: quantized as zeros
+    const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + (have ? src : 0) * src_bytes + (int64_t)j0 * kB;
+    uint2* codes = reinterpret_cast<uint2*>(p.codes) + (int64_t)row * p.nblk + j0;
+    const uint32_t pos = (uint32_t)tab.blk[g] * 128u + (row - (uint32_t)tab.off[g]);
+    uint8_t* scales = p.scales + (int64_t)((pos >> 7) * p.kc) * 512 + (uint32_t)(j0 >> 5) * 4096u + lane_scale +
+                      (pos & 31) * 16 + ((pos >> 5) & 3) * 4;
+    for (int j = j0; j < j_end; j += 32 * U) {
+      Block16<kF32> B[U], C[kGlu ? U : 1];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t b = base + u * 256;
-      if (b >= b_end) break;
-      const uint32_t row = div_u32(b, p.div_nblk);
-      const uint32_t j = b - row * p.nblk;
-      int64_t src = row;
-      if (p.row_index) src = __ldg(p.row_index + row);
-      B[u] = Block16<kF32>{};
-      if constexpr (kGlu) C[u] = Block16<kF32>{};
-      if (src >= 0 && src < p.M) {
-        const uint8_t* q = reinterpret_cast<const uint8_t*>(p.x) + (src * src_stride + j) * (kF32 ? 64 : 32);
-        load_block_wide<kF32>(q, B[u], p.wide != 0);
-        if constexpr (kGlu) load_block_wide<kF32>(q + (int64_t)p.nblk * (kF32 ? 64 : 32), C[u], p.wide != 0);
-      } else {
-        atomicCAS(p.err, 0u, kErrBounds);       // a row that x does not have: quantized as zeros
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t b = base + u * 256;
-      if (b >= b_end) break;
-      const uint32_t row = div_u32(b, p.div_nblk);
-      const uint32_t j = b - row * p.nblk;
-      if ((int)row >= tab.off[g + 1]) {
-        do ++g;
-        while ((int)row >= tab.off[g + 1]);
-        gs = __ldg(p.gs + g);
-      }
-      float f[16], amax;
-      block_floats<kF32>(B[u], f);
-      if constexpr (kGlu) {
-        float up[16];
-        block_floats<kF32>(C[u], up);
-        amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          f[i] = f[i] * __frcp_rn(1.0f + expf(-f[i])) * up[i];
-          amax = fmaxf(amax, fabsf(f[i]));
-        }
-      } else {
-        amax = block_amax<kF32>(B[u]);
-      }
-      uint32_t lo, hi;
-      const uint32_t s = quantize_values(f, amax, gs, lo, hi);
-      if (bounds_ok((uint64_t)(b + 1) * 8 <= p.codes_bytes, p.err))
-        reinterpret_cast<uint2*>(p.codes)[b] = make_uint2(lo, hi);
-      const int64_t pos = (int64_t)tab.blk[g] * 128 + ((int)row - tab.off[g]);
-      const int64_t o = tc_scale_offset(pos, j, p.kc);
-      if (bounds_ok((uint64_t)o < p.scale_bytes, p.err)) p.scales[o] = (uint8_t)s;
-      // K % 64 == 32: the row's last chunk has two padding slots
-      if (j == p.nblk - 1 && (p.nblk & 3) == 2) {
-        const int64_t o2 = tc_scale_offset(pos, j + 2, p.kc);
-        if (bounds_ok((uint64_t)o2 < p.scale_bytes, p.err)) {
-          p.scales[o2 - 1] = 0;
-          p.scales[o2] = 0;
+      for (int u = 0; u < U; ++u) {
+        B[u] = Block16<kF32>{};
+        if constexpr (kGlu) C[u] = Block16<kF32>{};
+        if (j + 32 * u < j_end && have) {
+          load_block_wide<kF32>(x + 32 * kB * u, B[u], wide);
+          if constexpr (kGlu) load_block_wide<kF32>(x + 32 * kB * u + (int64_t)p.nblk * kB, C[u], wide);
         }
       }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int ju = j + 32 * u;
+        if (ju >= j_end) break;
+        float f[16], amax;
+        block_floats<kF32>(B[u], f);
+        if constexpr (kGlu) {
+          float up[16];
+          block_floats<kF32>(C[u], up);
+          amax = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            f[i] = silu(f[i]) * up[i];
+            amax = fmaxf(amax, fabsf(f[i]));
+          }
+        } else {
+          amax = block_amax<kF32>(B[u]);
+        }
+        uint32_t lo, hi;
+        const uint32_t s = quantize_values(f, amax, gs, q, lo, hi);
+        if (bounds_ok((uint64_t)((int64_t)row * p.nblk + ju + 1) * 8 <= p.codes_bytes, p.err))
+          codes[32 * u] = make_uint2(lo, hi);
+        uint8_t* sc = scales + 4096 * u;
+        if (bounds_ok((uint64_t)(sc - p.scales) < p.scale_bytes, p.err)) *sc = (uint8_t)s;
+        // K % 64 == 32: the row's last chunk has two padding slots
+        if (ju == p.nblk - 1 && (p.nblk & 3) == 2 && bounds_ok((uint64_t)(sc + 2 - p.scales) < p.scale_bytes, p.err))
+          sc[1] = sc[2] = 0;
+      }
+      x += 32 * kB * U;
+      codes += 32 * U;
+      scales += 4096 * U;
     }
   }
 }
@@ -206,6 +227,7 @@ nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_a
   if (M < 1 || T < 1 || K < 32 || K % 32 != 0 || n_groups < 1) return NVFP4_ERR_INVALID_ARG;
   if (!row_index && M < T) return NVFP4_ERR_INVALID_ARG;
   if (n_groups > NVFP4_MAX_GROUPS || T > (1ll << 31) - 256 || M > (1ll << 31) - 256 || K > (1ll << 31) ||
+      grouped_blocks(T, n_groups) * 128 >= (1ll << 32) || grouped_blocks(T, n_groups) * ceil_div(K, 64) >= (1ll << 32) ||
       T * (K / 16) >= (1ll << 31) - (1ll << 20))
     return NVFP4_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(block_scales)) return NVFP4_ERR_ALIGNMENT;
@@ -220,18 +242,22 @@ nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_a
   p.offsets = group_offsets;
   p.E = n_groups;
   p.T = T;
-  p.nblk = (uint32_t)(K / 16);
-  p.div_nblk = make_div(p.nblk);
+  // a warp an item: whole rows if they give every SM some 32 warps, else parts
+  // of them
+  p.nblk = (int)(K / 16);
+  const int64_t nseg = ceil_div(p.nblk, 32), warps = (int64_t)d->sm_count * 32;
+  p.seg = (int)(T * nseg / warps < 1 ? 1 : T * nseg / warps < nseg ? T * nseg / warps : nseg);
+  p.parts = (int)ceil_div(nseg, p.seg);
+  p.div_parts = make_div((uint32_t)p.parts);
   p.gs = global_scales;
   p.codes = codes;
   p.scales = block_scales;
-  p.kc = ceil_div(K, 64);
+  p.kc = (uint32_t)ceil_div(K, 64);
   p.codes_bytes = (uint64_t)T * (uint64_t)(K / 2);
   p.scale_bytes = nvfp4_grouped_scale_bytes(T, n_groups, K);
   p.wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
   p.err = d->err_word;
-  const int64_t want = ceil_div(T * (K / 16), 256);
-  const int64_t cap = (int64_t)d->sm_count * 8;
+  const int64_t want = ceil_div(T * p.parts, 8), cap = (int64_t)d->sm_count * QCTAS;
   const int grid = (int)(want < cap ? want : cap);
   cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = dtype == NVFP4_IN_F32, glu = act == NVFP4_ACT_SWIGLU;

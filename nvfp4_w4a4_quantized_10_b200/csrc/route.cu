@@ -11,8 +11,8 @@
 // microsecond or two at any size met in serving.
 //
 // Selection: one warp a token, each lane holding E / 32 logits as ordered
-// 32-bit keys; a round is one warp-wide integer maximum for the key and one
-// minimum for the index (redux), so ties need no extra pass.
+// 32-bit keys; a round is one warp-wide integer maximum for the key and, for
+// FP32 logits, one minimum for the index (redux), so ties need no extra pass.
 // Sort: an expert is taken at most once by a token, so the rank of (m, e) is
 // a population count: 128 tokens set one bit each in a 128-bit mask of every
 // expert (an OR is order-free, so the result does not depend on timing), and
@@ -46,15 +46,15 @@ struct RouteParams {
   int32_t* slots;
   int32_t* row_index;
   int32_t* offsets;
-  int32_t* hist;         // [chunks, E] pairs of each run of tokens
+  int32_t* hist;         // [chunks, hist_stride(E)] pairs of each run of tokens
   int64_t chunk;         // tokens of a run
 };
 
-// Order-preserving key of a finite float; 0 for an expert that must not be
-// taken (-inf, NaN).  -0 counts as +0.
+// Order-preserving 32-bit key of a logit, 0 for an expert that must not be
+// taken (-inf, NaN); -0 counts as +0, +inf as the largest float.
 __device__ __forceinline__ uint32_t order_key(float x) {
   if (!(x > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
+  const uint32_t b = __float_as_uint(fminf(__fadd_rn(x, 0.0f), FLT_MAX));
   return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
@@ -62,35 +62,47 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-template <bool kF32>
-__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  float x;
-  if constexpr (kF32) x = __ldg(reinterpret_cast<const float*>(p) + i);
-  else x = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << 16);
-  return x == INFINITY ? FLT_MAX : x;
+// bf16 logits: the key's upper half says all (the largest bf16 stands for
+// +inf), and the lower half holds the index, inverted, so that one maximum
+// finds value and lowest index together.
+__device__ __forceinline__ uint32_t order_key_bf16(float x, int e) {
+  if (!(x > -INFINITY)) return 0u;
+  const uint32_t b = __float_as_uint(fminf(__fadd_rn(x, 0.0f), __uint_as_float(0x7F7F0000u)));
+  return ((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)e);
 }
 
-// Exclusive prefix of `total` over the experts, by thread index (E <=
-// blockDim.x): offset of expert threadIdx.x; `sum` the grand total.
-__device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int& sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
+// Value of a key: bf16 keys of negative numbers have their lower half set.
+template <bool kF32>
+__device__ __forceinline__ float selected_value(uint32_t k) {
+  if constexpr (kF32) return key_value(k);
+  else return key_value(k & 0x80000000u ? k & 0xFFFF0000u : k | 0xFFFFu);
+}
+
+template <bool kF32>
+__device__ __forceinline__ float load_logit(const void* p, int64_t i) {
+  if constexpr (kF32) return __ldg(reinterpret_cast<const float*>(p) + i);
+  else return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << 16);
+}
+
+// Experts in a row of the counts of all runs: rows start on 16 bytes.
+__host__ __device__ constexpr int hist_stride(int E) { return (E + 3) & ~3; }
+
+// By one warp: v[e] becomes the sum of v[0 .. e - 1]; returns the total.
+__device__ __forceinline__ int warp_exclusive(int* v, int E) {
+  const int lane = threadIdx.x & 31;
+  int carry = 0;
+  for (int base = 0; base < E; base += 32) {
+    const int own = base + lane < E ? v[base + lane] : 0;
+    int s = own;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int u = __shfl_up_sync(0xFFFFFFFFu, s, d);
-    if (lane >= d) s += u;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(0xFFFFFFFFu, s, d);
+      if (lane >= d) s += u;
+    }
+    if (base + lane < E) v[base + lane] = carry + s - own;
+    carry += __shfl_sync(0xFFFFFFFFu, s, 31);
   }
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int before = 0;
-  sum = 0;
-  for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-    const int u = warp_sums[w];
-    if (w < warp) before += u;
-    sum += u;
-  }
-  __syncthreads();
-  return before + s - v;
+  return carry;
 }
 
 template <bool kF32, int NV>
@@ -98,7 +110,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
   __shared__ uint32_t mask[kMaxGroups][kSub / 32];
   __shared__ int count[kMaxGroups];
   __shared__ int16_t ids_s[kSub * kMaxTopK];
-  __shared__ int warp_sums[kRouteWarps];
+  __shared__ int total_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = p.E, k = p.k;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -122,50 +134,53 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
     load_token(warp);
     for (int ml = warp; ml < n; ml += kRouteWarps) {
       const int64_t m = sub + ml;
-      uint32_t key[NV];
+      uint32_t key[NV], best = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = order_key(x[i]);
+      for (int i = 0; i < NV; ++i) {
+        key[i] = kF32 ? order_key(x[i]) : order_key_bf16(x[i], lane + 32 * i);
+        best = max(best, key[i]);
+      }
       load_token(ml + kRouteWarps);
-      // softmax over all experts: the sum before any is taken out
-      uint32_t best = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) best = max(best, key[i]);
       const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-      const float x_max = top ? key_value(top) : 0.0f;
+      const float x_max = top ? selected_value<kF32>(top) : 0.0f;
       float sum = 0.0f;
-      if (!p.renorm) {
+      if (!p.renorm) {                           // over all experts, before any is taken out
 #pragma unroll
-        for (int i = 0; i < NV; ++i) sum += key[i] ? expf(key_value(key[i]) - x_max) : 0.0f;
+        for (int i = 0; i < NV; ++i) sum += key[i] ? expf(selected_value<kF32>(key[i]) - x_max) : 0.0f;
       }
+      uint32_t my_key = 0;                       // lane j keeps the j-th selected
       int my_id = -1;
-      float my_e = 0.0f;
       for (int j = 0; j < k; ++j) {
-        const uint32_t kmax = __reduce_max_sync(0xFFFFFFFFu, best);
+        const uint32_t kmax = j == 0 ? top : __reduce_max_sync(0xFFFFFFFFu, best);
         if (kmax == 0) break;                    // nothing left that may be taken
-        uint32_t at = 0xFFFFFFFFu;
+        int at;
+        if constexpr (kF32) {
+          uint32_t own = 0xFFFFFFFFu;
 #pragma unroll
-        for (int i = NV - 1; i >= 0; --i)
-          if (key[i] == kmax) at = lane + 32 * i;
-        at = __reduce_min_sync(0xFFFFFFFFu, at);
-        if (lane == j) {
-          my_id = (int)at;
-          my_e = expf(key_value(kmax) - x_max);
+          for (int i = NV - 1; i >= 0; --i)
+            if (key[i] == kmax) own = lane + 32 * i;
+          at = (int)__reduce_min_sync(0xFFFFFFFFu, own);
+        } else {
+          at = 0xFFFF - (int)(kmax & 0xFFFFu);
         }
-        if ((at & 31) == (uint32_t)lane) {
-          best = 0;
+        if (lane == j) {
+          my_id = at;
+          my_key = kmax;
+        }
+        best = 0;
 #pragma unroll
-          for (int i = 0; i < NV; ++i) {
-            if (lane + 32 * i == (int)at) key[i] = 0;
-            best = max(best, key[i]);
-          }
+        for (int i = 0; i < NV; ++i) {
+          if (kF32 ? lane + 32 * i == at : key[i] == kmax) key[i] = 0;
+          best = max(best, key[i]);
         }
       }
+      const float my_e = my_id >= 0 ? expf(selected_value<kF32>(my_key) - x_max) : 0.0f;
       if (p.renorm) sum = my_e;
 #pragma unroll
       for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
       if (lane < k) {
         p.ids[m * k + lane] = my_id;
-        p.weights[m * k + lane] = my_id >= 0 ? __fdiv_rn(my_e, sum) : 0.0f;
+        p.weights[m * k + lane] = my_id >= 0 ? __fmul_rn(my_e, __frcp_rn(sum)) : 0.0f;
         ids_s[ml * k + lane] = (int16_t)my_id;
         if (my_id >= 0) atomicOr(&mask[my_id][ml >> 5], 1u << (ml & 31));
       }
@@ -194,18 +209,17 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
     __syncthreads();
   }
   if (gridDim.x > 1) {
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * E + e] = count[e];
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * hist_stride(E) + e] = count[e];
     return;
   }
   // the only CTA: ranks become slots here
-  int total;
-  const int off = block_exclusive((int)threadIdx.x < E ? count[threadIdx.x] : 0, warp_sums, total);
-  if ((int)threadIdx.x < E) {
-    count[threadIdx.x] = off;
-    p.offsets[threadIdx.x] = off;
+  if (warp == 0) {
+    const int t = warp_exclusive(count, E);
+    if (lane == 0) total_s = t;
   }
-  if (threadIdx.x == 0) p.offsets[E] = total;
   __syncthreads();
+  const int total = total_s;
+  for (int e = threadIdx.x; e <= E; e += kRouteThreads) p.offsets[e] = e < E ? count[e] : total;
   const int pairs = (int)(p.M * k);
   for (int i = threadIdx.x; i < pairs; i += kRouteThreads) {
     const int e = p.ids[i];
@@ -220,15 +234,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
 
 // Second launch of a call with more than one run of tokens: every CTA adds up
 // all runs' counts (for the offsets) and those before its own (for its base),
-// then turns its ranks into slots.  E <= blockDim.x; blockDim.x / ep threads
-// share an expert, ep the power of two >= E.
-__global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteParams p, int ep) {
-  __shared__ int part[2][kRouteThreads];
-  __shared__ int base[kMaxGroups];
-  __shared__ int warp_sums[kRouteWarps];
+// four experts a thread and load, then turns its ranks into slots.
+__global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteParams p) {
+  __shared__ int all[kMaxGroups + 3];
+  __shared__ int before[kMaxGroups + 3];
+  __shared__ int total_s;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int E = p.E, k = p.k, stride = hist_stride(E);
+  for (int e = threadIdx.x; e < stride; e += kRouteThreads) all[e] = before[e] = 0;
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int E = p.E, k = p.k;
   const int64_t m_begin = (int64_t)blockIdx.x * p.chunk;
   const int64_t m_end = m_begin + p.chunk < p.M ? m_begin + p.chunk : p.M;
   const int i_end = (int)(m_end * k);
@@ -239,39 +254,46 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
     id = __ldg(p.ids + i);
     rank = p.slots[i];
   }
-  const int e = threadIdx.x & (ep - 1), q = threadIdx.x / ep, parts = kRouteThreads / ep;
-  int all = 0, before = 0;
-  if (e < E) {
-#pragma unroll 8
-    for (int c = q; c < (int)gridDim.x; c += parts) {
-      const int h = __ldg(p.hist + (int64_t)c * E + e);
-      all += h;
-      if (c < (int)blockIdx.x) before += h;
+  const int quads = stride / 4, at = threadIdx.x % quads, rows = kRouteThreads / quads;
+  int4 sum = make_int4(0, 0, 0, 0), head = make_int4(0, 0, 0, 0);
+  if ((int)threadIdx.x < rows * quads) {
+#pragma unroll 4
+    for (int c = threadIdx.x / quads; c < (int)gridDim.x; c += rows) {
+      const int4 h = __ldg(reinterpret_cast<const int4*>(p.hist + (int64_t)c * stride) + at);
+      sum.x += h.x;
+      sum.y += h.y;
+      sum.z += h.z;
+      sum.w += h.w;
+      if (c < (int)blockIdx.x) {
+        head.x += h.x;
+        head.y += h.y;
+        head.z += h.z;
+        head.w += h.w;
+      }
     }
+    atomicAdd(&all[4 * at], sum.x);              // integer sums: any order gives the same
+    atomicAdd(&all[4 * at + 1], sum.y);
+    atomicAdd(&all[4 * at + 2], sum.z);
+    atomicAdd(&all[4 * at + 3], sum.w);
+    atomicAdd(&before[4 * at], head.x);
+    atomicAdd(&before[4 * at + 1], head.y);
+    atomicAdd(&before[4 * at + 2], head.z);
+    atomicAdd(&before[4 * at + 3], head.w);
   }
-  part[0][threadIdx.x] = all;
-  part[1][threadIdx.x] = before;
   __syncthreads();
-  all = before = 0;
-  if ((int)threadIdx.x < E) {
-    for (int i = 0; i < parts; ++i) {
-      all += part[0][i * ep + threadIdx.x];
-      before += part[1][i * ep + threadIdx.x];
-    }
+  if (threadIdx.x < 32) {
+    const int t = warp_exclusive(all, E);
+    if (threadIdx.x == 0) total_s = t;
   }
-  int total;
-  const int off = block_exclusive(all, warp_sums, total);
-  if ((int)threadIdx.x < E) {
-    base[threadIdx.x] = off + before;
-    if (blockIdx.x == 0) p.offsets[threadIdx.x] = off;
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[E] = total;
   __syncthreads();
+  const int total = total_s;
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= E; e += kRouteThreads) p.offsets[e] = e < E ? all[e] : total;
   while (i < i_end) {
     if (id >= 0) {
-      const int at = base[id] + rank;
-      p.slots[i] = at;
-      p.row_index[at] = i / k;
+      const int slot = all[id] + before[id] + rank;
+      p.slots[i] = slot;
+      p.row_index[slot] = i / k;
     }
     if (i >= total) p.row_index[i] = -1;         // rows no pair fills
     i += kRouteThreads;
@@ -284,10 +306,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
 
 namespace {
 
-// Runs of tokens: one CTA up to 64 tokens (2 a warp: one launch), else at
+// Runs of tokens: one CTA and one launch up to 32 tokens, one a warp (64 tokens
+// that way took 7.9 us, as two runs and two launches 6.9), else at
 // least 32 tokens a run, one for each warp, and at most one run an SM.
 int64_t route_chunks(int64_t M, int sms) {
-  if (M <= 64) return 1;
+  if (M <= kRouteWarps) return 1;
   const int64_t cap = sms < kRouteMaxChunks ? sms : kRouteMaxChunks;
   const int64_t c = ceil_div(M, kRouteWarps);
   return c < cap ? c : cap;
@@ -312,7 +335,7 @@ extern "C" {
 
 size_t nvfp4_route_workspace_bytes(int n_experts) {
   if (n_experts < 1 || n_experts > NVFP4_MAX_GROUPS) return 0;
-  return (size_t)kRouteMaxChunks * (size_t)n_experts * sizeof(int32_t);
+  return (size_t)kRouteMaxChunks * (size_t)hist_stride(n_experts) * sizeof(int32_t);
 }
 
 nvfp4_status nvfp4_route(const void* logits, nvfp4_in_dtype dtype, int64_t M, int n_experts, int top_k,
@@ -349,11 +372,7 @@ nvfp4_status nvfp4_route(const void* logits, nvfp4_in_dtype dtype, int64_t M, in
   const int grid = (int)ceil_div(M, p.chunk);
   cudaStream_t st = (cudaStream_t)stream;
   cudaError_t e = dtype == NVFP4_IN_F32 ? launch_topk<true>(p, grid, st) : launch_topk<false>(p, grid, st);
-  if (e == cudaSuccess && grid > 1) {
-    int ep = 32;
-    while (ep < n_experts) ep *= 2;
-    e = launch_pdl(route_slots_kernel, grid, kRouteThreads, st, p, ep);
-  }
+  if (e == cudaSuccess && grid > 1) e = launch_pdl(route_slots_kernel, grid, kRouteThreads, st, p);
   return cuda_status(e);
 }
 
