@@ -25,10 +25,6 @@ namespace nvfp4 {
 
 constexpr int kNormMaxK = 32768;
 
-// Most threads of a CTA whose threads own NB 16-element blocks: K up to 8192,
-// 18432 and 32768.
-constexpr int norm_threads(int nb) { return nb == 2 ? 576 : 512; }
-
 struct NormParams {
   const void* y;
   int64_t M, K, y_rows;
@@ -108,8 +104,11 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // every SM's loads coming while other rows wait in their reductions (16384 x
 // 5120 bf16, residual and norm: 121 us; a persistent grid of 2, 3, 4 or 6 CTAs
 // an SM that walks the rows: 143, 168, 129, 148).
-template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate>
-__global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const NormParams p) {
+// kThreads, kCtas: the CTA's most threads, and CTAs that are to fit on an SM
+// (which caps the registers; 48 of them instead of 56 are 4 CTAs instead of 3
+// and 99 instead of 108 us in that case).
+template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormParams p) {
   __shared__ float red[2][32];
   __shared__ float quot[8];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -262,13 +261,12 @@ __global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const Norm
       }
       if constexpr (kGate) {
         block_floats<kF32>(gb, x);
+        if (p.gate_kind == NVFP4_GATE_LINEAR) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float a = x[i];
-          if (p.gate_kind != NVFP4_GATE_LINEAR) {
-            a = p.gate_kind == NVFP4_GATE_SILU ? silu(x[i]) : sigmoid(x[i]);
-          }
-          f[b][i] *= a;
+          for (int i = 0; i < 16; ++i) f[b][i] *= x[i];
+        } else {
+          if (p.gate_kind == NVFP4_GATE_SILU) apply_gate<true>(x, f[b]);
+          else apply_gate<false>(x, f[b]);
         }
       }
       block_floats<kF32>(rb, x);
@@ -336,29 +334,36 @@ __global__ void __launch_bounds__(norm_threads(NB)) block_norm_kernel(const Norm
 
 namespace {
 
-template <bool kF32, int NB, bool kWarpRow>
+// kCtas of the kernel without slots and gate; those hold more and get fewer.
+template <bool kF32, int NB, bool kWarpRow, int kThreads, int kCtas>
 cudaError_t launch_norm_as(const NormParams& p, int grid, int threads, cudaStream_t st) {
+  constexpr int kGated = kCtas > 3 ? 3 : kCtas, kSlotted = kCtas > 2 ? 2 : kCtas;
   if (p.slots)
-    return p.gate ? launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, true, true>, grid, threads, st, p)
-                  : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, true, false>, grid, threads, st, p);
-  return p.gate ? launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, true>, grid, threads, st, p)
-                : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, false>, grid, threads, st, p);
+    return p.gate
+               ? launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, true, true, kThreads, kSlotted>, grid, threads, st, p)
+               : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, true, false, kThreads, kSlotted>, grid, threads, st, p);
+  return p.gate
+             ? launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, true, kThreads, kGated>, grid, threads, st, p)
+             : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, false, kThreads, kCtas>, grid, threads, st, p);
 }
 
+// Rows of at most 1024 elements: a warp each, 8 to a CTA.  Longer ones: a CTA
+// each, with one 16-element block a thread while registers allow (K up to
+// 8192), then two (18432), then four.
 template <bool kF32>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
   const int nblk = (int)(p.K / 16);
-  // rows of at most 1024: a warp each, 8 to a CTA; longer ones a CTA each
   if (nblk <= 64) {
     const int grid = (int)ceil_div(p.M, 8);
-    return nblk <= 32 ? launch_norm_as<kF32, 1, true>(p, grid, 256, st) : launch_norm_as<kF32, 2, true>(p, grid, 256, st);
+    return nblk <= 32 ? launch_norm_as<kF32, 1, true, 256, 4>(p, grid, 256, st)
+                      : launch_norm_as<kF32, 2, true, 256, 3>(p, grid, 256, st);
   }
-  const int nb = nblk <= norm_threads(1) ? 1 : nblk <= 2 * norm_threads(2) ? 2 : 4;
-  const int threads = (int)ceil_div(ceil_div(nblk, nb), 32) * 32;
   const int grid = (int)p.M;
-  if (nb == 1) return launch_norm_as<kF32, 1, false>(p, grid, threads, st);
-  if (nb == 2) return launch_norm_as<kF32, 2, false>(p, grid, threads, st);
-  return launch_norm_as<kF32, 4, false>(p, grid, threads, st);
+  auto threads = [&](int nb) { return (int)ceil_div(ceil_div(nblk, nb), 32) * 32; };
+  if (nblk <= 320) return launch_norm_as<kF32, 1, false, 320, 4>(p, grid, threads(1), st);
+  if (nblk <= 512) return launch_norm_as<kF32, 1, false, 512, 2>(p, grid, threads(1), st);
+  if (nblk <= 2 * 576) return launch_norm_as<kF32, 2, false, 576, 2>(p, grid, threads(2), st);
+  return launch_norm_as<kF32, 4, false, 512, 1>(p, grid, threads(4), st);
 }
 
 }  // namespace

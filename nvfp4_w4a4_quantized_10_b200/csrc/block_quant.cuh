@@ -288,9 +288,30 @@ __device__ __forceinline__ uint32_t quantize_values(const float (&f)[16], float 
   return s;
 }
 
-// f * sigmoid(f) and sigmoid(f): exp to 2 ulp, one approximate quotient (2
-// ulp; its flush to zero beyond 2^126 is the limit's own value).
-__device__ __forceinline__ float silu(float f) { return __fdividef(f, 1.0f + expf(-f)); }
-__device__ __forceinline__ float sigmoid(float f) { return __fdividef(1.0f, 1.0f + expf(-f)); }
+// f_i *= num_i / (1 + exp(-x_i)): a sigmoid (num = 1) or SiLU (num = x) gate
+// of a block.  The special-function unit is what gates cost (a warp's exp or
+// reciprocal holds it for 8 cycles), so two quotients share a reciprocal,
+// 1 / a = b * (1 / (a b)), which holds while the product stays finite: for
+// x >= -43 throughout the block.  exp to 2 ulp, reciprocal 1 ulp, a few
+// products.
+template <bool kSilu>
+__device__ __forceinline__ void apply_gate(const float (&x)[16], float (&f)[16]) {
+  float low = x[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) low = fminf(low, x[i]);
+  if (low >= -43.0f) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const float a = 1.0f + expf(-x[i]), b = 1.0f + expf(-x[i + 1]);
+      const float r = __fdividef(1.0f, __fmul_rn(a, b));
+      f[i] *= kSilu ? x[i] * (b * r) : b * r;
+      f[i + 1] *= kSilu ? x[i + 1] * (a * r) : a * r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)       // flushed to zero beyond 2^126: the limit's own value
+      f[i] *= __fdividef(kSilu ? x[i] : 1.0f, 1.0f + expf(-x[i]));
+  }
+}
 
 }  // namespace nvfp4

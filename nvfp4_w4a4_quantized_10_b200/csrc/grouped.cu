@@ -17,9 +17,6 @@
 #include "groups.cuh"
 #include "ptx.cuh"
 
-#ifndef QCTAS
-#define QCTAS 6
-#endif
 namespace nvfp4 {
 
 struct GroupedQuantParams {
@@ -50,11 +47,13 @@ struct GroupedQuantParams {
 // groups, and the scale quotients of the groups it meets, once.
 // Bound: HBM writes 9/16 byte an element and reads each source row once, but a
 // row gathered k times is read k - 1 times from L2 and encoded k times, and
-// the encoding (some 100 instructions a block) is what it waits for: 2048 rows
-// of 5120 gathered 8 times took 42 us with a flat loop over blocks (214
-// instructions each).
+// the encoding (some 140 instructions a block) is what it waits for: 2048 rows
+// of 5120 gathered 8 times take 31 us, and took 42 with a flat loop over blocks
+// (214 instructions each); 16384 rows once, 37 us (5.8 TB/s).
+constexpr int kQuantCtas = 3;   // CTAs an SM: all resident, one prologue each (4 of them: 33.1 against 31.4 us, 6 in two waves: 37)
+
 template <bool kF32, bool kGlu>
-__global__ void __launch_bounds__(256) grouped_quantize_kernel(const GroupedQuantParams p) {
+__global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const GroupedQuantParams p) {
   __shared__ GroupTable tab;
   __shared__ float quot[kMaxGroups][8];
   constexpr int U = kF32 || kGlu ? 2 : 4;                 // loads in flight
@@ -115,10 +114,11 @@ __global__ void __launch_bounds__(256) grouped_quantize_kernel(const GroupedQuan
         if constexpr (kGlu) {
           float up[16];
           block_floats<kF32>(C[u], up);
+          apply_gate<true>(f, up);
           amax = 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            f[i] = silu(f[i]) * up[i];
+            f[i] = up[i];
             amax = fmaxf(amax, fabsf(f[i]));
           }
         } else {
@@ -257,7 +257,7 @@ nvfp4_status nvfp4_grouped_quantize(const void* x, nvfp4_in_dtype dtype, nvfp4_a
   p.scale_bytes = nvfp4_grouped_scale_bytes(T, n_groups, K);
   p.wide = (reinterpret_cast<uintptr_t>(x) & 31) == 0;
   p.err = d->err_word;
-  const int64_t want = ceil_div(T * p.parts, 8), cap = (int64_t)d->sm_count * QCTAS;
+  const int64_t want = ceil_div(T * p.parts, 8), cap = (int64_t)d->sm_count * kQuantCtas;
   const int grid = (int)(want < cap ? want : cap);
   cudaStream_t st = (cudaStream_t)stream;
   const bool f32 = dtype == NVFP4_IN_F32, glu = act == NVFP4_ACT_SWIGLU;
