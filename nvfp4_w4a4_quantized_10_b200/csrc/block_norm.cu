@@ -321,7 +321,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
       }
     }
   }
-  // padding rows of the tensor-core layout (up to 127 past M): zero scales
+  // padding rows of the tensor-core layout (up to 127 past M): zero scales,
+  // one row a CTA
   if (p.codes && p.tc_layout) {
     const int64_t end = (p.M + 127) / 128 * 128;
     for (int64_t r = p.M + blockIdx.x; r < end; r += gridDim.x)
@@ -353,12 +354,14 @@ cudaError_t launch_norm_as(const NormParams& p, int grid, int threads, cudaStrea
 template <bool kF32>
 cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
   const int nblk = (int)(p.K / 16);
+  const int64_t padding = p.codes && p.tc_layout ? ceil_div(p.M, 128) * 128 - p.M : 0;
+  auto ctas = [&](int64_t rows) { return (int)(rows > padding ? rows : padding); };
   if (nblk <= 64) {
-    const int grid = (int)ceil_div(p.M, 8);
+    const int grid = ctas(ceil_div(p.M, 8));
     return nblk <= 32 ? launch_norm_as<kF32, 1, true, 256, 4>(p, grid, 256, st)
                       : launch_norm_as<kF32, 2, true, 256, 3>(p, grid, 256, st);
   }
-  const int grid = (int)p.M;
+  const int grid = ctas(p.M);
   auto threads = [&](int nb) { return (int)ceil_div(ceil_div(nblk, nb), 32) * 32; };
   if (nblk <= 320) return launch_norm_as<kF32, 1, false, 320, 4>(p, grid, threads(1), st);
   if (nblk <= 512) return launch_norm_as<kF32, 1, false, 512, 2>(p, grid, threads(1), st);

@@ -58,14 +58,14 @@ inline bool make_sf_map(CUtensorMap* m, const void* base, int64_t rows, int64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Output [M, N] (bf16 or f32), boxes of 128 rows x 128 bytes, 128B swizzle.
-inline bool make_out_map(CUtensorMap* m, void* base, int64_t M, int64_t N, bool f32) {
+// Output [M, N] (bf16 or f32), boxes of box_rows rows x 128 bytes, 128B swizzle.
+inline bool make_out_map(CUtensorMap* m, void* base, int64_t M, int64_t N, bool f32, int box_rows = kBM) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const int64_t esz = f32 ? 4 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)N, (cuuint64_t)M};
   const cuuint64_t strides[1] = {(cuuint64_t)(N * esz)};
-  const cuuint32_t box[2] = {(cuuint32_t)(128 / esz), (cuuint32_t)kBM};
+  const cuuint32_t box[2] = {(cuuint32_t)(128 / esz), (cuuint32_t)box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     fence_barrier_init();
     prefetch_tmap(&p.tmap_p);
     prefetch_tmap(&p.tmap_q);
-    if (!SWAP && !GROUPED && p.tma_store) prefetch_tmap(&p.tmap_out);
+    if (!SWAP && p.tma_store) prefetch_tmap(&p.tmap_out);
     if (PAIR) {
       prefetch_tmap(&p.tmap_sfa);
       prefetch_tmap(&p.tmap_sfb);
@@ -1016,37 +1016,55 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       tc_fence_after();
       if constexpr (GROUPED && PAIR) {
         // Lane = weight row = output column n, accumulator column = activation
-        // row, as in swapped tiles: 64 (FP32 output: 32) rows at a time go
-        // through a 16 KB buffer as [row][128 columns] and out in 16-byte
-        // pieces, masked by the group's end, so no row of a neighbour is
-        // touched.  A buffer is rewritten only after a barrier that follows
-        // its last reads.
+        // row: the tile leaves transposed.  64 rows at a time (FP32 output: 32)
+        // go through a 16 KB buffer of 128-byte-wide, 128B-swizzled sub-tiles
+        // [rows][64 or 32 columns] and out as TMA stores, which clip at N; the
+        // rows of a slot that runs past the group are stored one by one
+        // instead, so no row of a neighbour is touched.  bf16 is transposed on
+        // the way in (fragment loads from TMEM, stmatrix.trans): element
+        // stores and loads cost 2900 cycles a slot, more than the MMAs of a
+        // tile with K = 1024.
         const uint32_t tacc = taddr + (acc_buf ? C::kAcc1Col : 0);
         auto slot_col = [&](int slot) -> int {
           return C::kOverlapAcc && acc_buf == 0 ? ((slot + 4 - C::kSharedSlots) & 3) * 64 : slot * 64;
         };
         constexpr int kEsz = OUT_F32 ? 4 : 2;
+        constexpr int kRows = OUT_F32 ? 32 : 64;      // activation rows of a buffer
+        constexpr int kSubCols = 128 / kEsz;          // output columns of a sub-tile
+        constexpr int kSubBytes = kRows * 128;
         const bool vec = p.tma_store != 0;            // output rows start on 16-byte boundaries
-        // a buffer is rewritten after a barrier that follows its last reads:
-        // with two, the other one's
+        // the next buffer, once its last store has read it and every thread
+        // is done with it
         auto next_buf = [&]() {
-          if (C::kOutBufs == 1) named_bar_sync(kEpiBar, 128);
-          else out_buf ^= 1;
-          return sbase + C::kOffOut + (C::kOutBufs == 1 ? 0 : out_buf) * kStageOutBytes;
-        };
-        auto flush = [&](uint32_t buf, int col) {     // a staged buffer, rows col ... of the tile
+          if (C::kOutBufs == 2) out_buf ^= 1;
+          if (et == 0) bulk_wait_group_read<C::kOutBufs - 1>();
           named_bar_sync(kEpiBar, 128);
+          return sbase + C::kOffOut + out_buf * kStageOutBytes;
+        };
+        auto flush = [&](uint32_t buf, int col) {     // a filled buffer, rows col ... of the tile
+          const bool whole = vec && col + kRows <= w.rows;
+          if (whole) fence_proxy_async_smem();
+          named_bar_sync(kEpiBar, 128);
+          if (whole) {
+            if (et == 0) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int id = et + 128 * j;
-            const int r = id / (8 * kEsz), ch = id % (8 * kEsz);
-            const int64_t n = p0 + ch * (16 / kEsz);
+              for (int sub = 0; sub < 128 / kSubCols; ++sub)
+                if (p0 + sub * kSubCols < N)
+                  tma_store_2d(&p.tmap_out, buf + sub * kSubBytes, (int32_t)(p0 + sub * kSubCols), (int32_t)(q0 + col));
+              bulk_commit_group();
+            }
+            return;
+          }
+#pragma unroll 1
+          for (int id = et; id < kStageOutBytes / 16; id += 128) {
+            const int sub = id / (kRows * 8), r = id / 8 % kRows, ch = id & 7;
+            const int64_t n = p0 + sub * kSubCols + ch * (16 / kEsz);
             if (col + r >= w.rows || n >= N) continue;
             const int64_t o = (q0 + col + r) * N + n;
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(buf + id * 16)
+                         : "r"(buf + sub * kSubBytes + swz128(r, ch))
                          : "memory");
             if (vec && n + 16 / kEsz <= N) {
               if (bounds_ok((uint64_t)(o + 16 / kEsz) <= p.out_elems, p.err))
@@ -1063,15 +1081,13 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
           }
         };
         if constexpr (!OUT_F32) {
-          // slots in drain order: the columns that the next accumulator shares
-          // go to registers, TMEM goes back, and only then does anything wait
-          // for the staging buffer
+          // v[16 h + 2 j + i]: lanes 16 h + 8 i ... of the warp, rows 8 j ...
           auto load_slot = [&](int col, uint32_t (&v)[32]) {
             if (col >= w.rows) return;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               uint32_t r[32];
-              tmem_ld_32x32b_x32(tacc + col + 32 * h, r);
+              tmem_ld_16x256b_x8(tacc + ((uint32_t)(16 * h) << 16) + col, r);
               tmem_ld_wait();
 #pragma unroll
               for (int i = 0; i < 16; ++i)
@@ -1079,20 +1095,20 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
                                             __fmul_rn(__uint_as_float(r[2 * i + 1]), g_alpha));
             }
           };
+          // this lane's stmatrix row: activation row lane % 8, output columns
+          // 8 (lane / 8) ... of the warp's 32
+          const uint32_t st_off = (uint32_t)(sp >> 1) * kSubBytes + swz128(lane & 7, (sp & 1) * 4 + (lane >> 3));
           auto store_slot = [&](int col, const uint32_t (&v)[32]) {
             if (col >= w.rows) return;
             const uint32_t buf = next_buf();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2 * i * 256 + row * 2),
-                           "h"((uint16_t)(v[i] & 0xFFFFu))
-                           : "memory");
-              asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + (2 * i + 1) * 256 + row * 2),
-                           "h"((uint16_t)(v[i] >> 16))
-                           : "memory");
-            }
+            for (int j = 0; j < 8; ++j)
+              stmatrix_x4_trans(buf + st_off + j * 1024, v[2 * j], v[2 * j + 1], v[16 + 2 * j], v[16 + 2 * j + 1]);
             flush(buf, col);
           };
+          // slots in drain order: the columns that the next accumulator shares
+          // go to registers, TMEM goes back, and only then does anything wait
+          // for a staging buffer
           static_assert(C::kSharedSlots == (BN == 256 ? 3 : 0), "slots drained before the accumulator goes back");
           uint32_t v0[32], v1[32];
           if constexpr (BN == 256) {
@@ -1129,8 +1145,8 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             if (!has) continue;
             const uint32_t buf = next_buf();
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + i * 512 + row * 4),
+            for (int i = 0; i < 32; ++i)              // the warp's 32 columns are sub-tile sp
+              asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + sp * kSubBytes + swz128(i, lane >> 2) + (lane & 3) * 4),
                            "f"(__fmul_rn(__uint_as_float(r[i]), g_alpha))
                            : "memory");
             flush(buf, col);
@@ -1407,7 +1423,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       acc_buf ^= 1;
       first_item = false;
     }
-    if (!GROUPED && tma_store && et == 0) bulk_wait_group<0>();   // stores done before the CTA's smem goes away
+    if (tma_store && et == 0) bulk_wait_group<0>();   // stores done before the CTA's smem goes away
   } else {
     // ------------------------------------------------------------ scale copies
     // warp 6 copies P's scale chunks of each stage into TMEM, warp 7 + rb the

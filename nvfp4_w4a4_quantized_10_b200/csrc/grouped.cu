@@ -114,11 +114,10 @@ __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const
         if constexpr (kGlu) {
           float up[16];
           block_floats<kF32>(C[u], up);
-          apply_gate<true>(f, up);
           amax = 0.0f;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            f[i] = up[i];
+            f[i] = silu(f[i]) * up[i];
             amax = fmaxf(amax, fabsf(f[i]));
           }
         } else {
@@ -196,7 +195,8 @@ nvfp4_status run_grouped_gemm(const uint8_t* a_codes, const uint8_t* a_scales, c
   p.kt = (int)ceil_div(K, 64 * C::kKB);
   p.tiles_p = (int)ceil_div(N, 256);
   p.group_p = C::kGroupTiles;
-  p.tma_store = (N * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;      // 16-byte stores reach every row
+  p.tma_store = (N * (f32 ? 4 : 2)) % 16 == 0 ? 1 : 0;      // output rows start on 16-byte boundaries
+  if (p.tma_store && !make_out_map(&p.tmap_out, out, T, N, f32, f32 ? 32 : 64)) return NVFP4_ERR_CUDA;
   if (!make_code_map(&p.tmap_p, w_codes, p.rows_p, K, kBM, C::kRowBytes)) return NVFP4_ERR_CUDA;
   for (int i = 0; i < 4; ++i)
     if (!make_code_map(&p.tmap_q_box[i], a_codes, T, K, 16 << i, C::kRowBytes)) return NVFP4_ERR_CUDA;
