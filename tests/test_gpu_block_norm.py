@@ -189,3 +189,52 @@ def test_on_another_stream_and_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def shifted(t):
+    """A copy of t that starts 16 bytes past a 32-byte boundary."""
+    n = 16 // t.element_size()
+    buf = torch.empty(t.numel() + 2 * n, dtype=t.dtype, device="cuda")
+    out = buf[n:n + t.numel()].view(t.shape).copy_(t)
+    assert out.data_ptr() % 32 == 16
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("K", [96, 1056, 9216])
+def test_buffers_on_16_byte_boundaries(K, dtype):
+    a = make(9, K, dtype, k=3, post=K, gate=nv.GATE_SILU)
+    b = {n: shifted(t) if torch.is_tensor(t) and t.is_floating_point() and n != "slot_weights" else t
+         for n, t in a.items()}
+    want, out = torch.empty(9, K, dtype=dtype, device="cuda"), shifted(torch.zeros(9, K, dtype=dtype, device="cuda"))
+    nv.nvfp4_block_norm(**a, out=want)
+    nv.nvfp4_block_norm(**b, out=out)
+    assert torch.equal(out, want)
+
+
+def test_gate_far_out_on_both_sides():
+    K = 64
+    y = torch.ones(1, K, device="cuda")
+    z = torch.linspace(-120.0, 120.0, K, device="cuda").view(1, K)
+    for kind in (nv.GATE_SIGMOID, nv.GATE_SILU):
+        out = torch.empty(1, K, device="cuda")
+        nv.nvfp4_block_norm(y, gate=z, gate_kind=kind, out=out)
+        d = z.double()
+        want = torch.sigmoid(d) * (d if kind == nv.GATE_SILU else 1.0)
+        # exp 2 ulp, quotient 2 ulp, a product; the exponent's own rounding is expf's; below 2^-126 flushed
+        assert ((out.double() - want).abs() <= 8 * ULP * want.abs() + 2.0 ** -125 * (1 + d.abs())).all()
+
+
+def test_more_than_2_31_elements():
+    M, K = 140_000, 16_384
+    y = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    rows = torch.randn(4, K, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    at = torch.tensor([0, 1, 131_073, M - 1], device="cuda")          # row 131072 starts at element 2^31
+    y.zero_()
+    y[at] = rows
+    w = torch.ones(K, device="cuda")
+    small = torch.empty(4, K, dtype=torch.bfloat16, device="cuda")
+    nv.nvfp4_block_norm(rows, pre_weight=w, out=small)
+    nv.nvfp4_block_norm(y, pre_weight=w, out=y)
+    assert torch.equal(y[at], small)
+    assert y[2].eq(0).all() and y[M - 2].eq(0).all()

