@@ -58,11 +58,13 @@ KERNEL_SOURCES = {
 
 
 def source_hash(kernel: str, read=None) -> str:
-    """Hash of one kernel's sources with // comments and blank lines removed,
-    so that a comment edit, or a change to another kernel, keeps its recorded
-    counters valid.  read(name) -> text overrides reading the working tree."""
+    """Hash of one kernel's sources, the headers of the same folder that they
+    include among them, with // comments and blank lines removed, so that a
+    comment edit, or a change to another kernel, keeps its recorded counters
+    valid.  read(name) -> text overrides reading the working tree."""
     h = hashlib.sha256()
-    for name in KERNEL_SOURCES[kernel]:
+    names = list(KERNEL_SOURCES[kernel])
+    for name in names:                      # grows as includes are met
         if read is None:
             with open(os.path.join(ROOT, "nvfp4_w4a4_quantized_10_b200", "csrc", name), encoding="utf-8") as f:
                 text = f.read()
@@ -72,6 +74,10 @@ def source_hash(kernel: str, read=None) -> str:
             code = line.split("//", 1)[0].rstrip()
             if code:
                 h.update(code.encode() + b"\n")
+            if code.startswith('#include "') and "/" not in code:
+                included = code.split('"')[1]
+                if included not in names:
+                    names.append(included)
     return h.hexdigest()[:16]
 
 
