@@ -1055,16 +1055,22 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             }
             return;
           }
+          // 16-byte pieces of the rows that the group has.  (One at a time: four
+          // in flight took registers from the slots that wait, and every tile
+          // paid for it, 136 instead of 108 us for 64 ragged groups of 250 rows
+          // against 5120 x 1024.)
+          constexpr int kPieces = 8 * 128 / kSubCols;           // of a row
+          const int n_ids = min(kRows, w.rows - col) * kPieces;
 #pragma unroll 1
-          for (int id = et; id < kStageOutBytes / 16; id += 128) {
-            const int sub = id / (kRows * 8), r = id / 8 % kRows, ch = id & 7;
-            const int64_t n = p0 + sub * kSubCols + ch * (16 / kEsz);
-            if (col + r >= w.rows || n >= N) continue;
+          for (int id = et; id < n_ids; id += 128) {
+            const int r = id / kPieces;
+            const int64_t n = p0 + id % kPieces * (16 / kEsz);
+            if (n >= N) continue;
             const int64_t o = (q0 + col + r) * N + n;
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                         : "r"(buf + sub * kSubBytes + swz128(r, ch))
+                         : "r"(buf + id / 8 % (kPieces / 8) * kSubBytes + swz128(r, id & 7))
                          : "memory");
             if (vec && n + 16 / kEsz <= N) {
               if (bounds_ok((uint64_t)(o + 16 / kEsz) <= p.out_elems, p.err))
