@@ -152,6 +152,8 @@ struct Cfg {
   // double-buffered; grouped tiles of BN = 128 give the second buffer to a
   // seventh stage (72.6 against 73.7 us for 2 rows of each of 64 experts)
   static constexpr int kOutBufs = GROUPED && BN == 128 ? 1 : 2;
+  // (Eight epilogue warps for grouped tiles of 256, on alternate tiles or on
+  // alternate slots: 10 % less time at K = 512, 3 % more at K >= 2048.)
   static constexpr int kOutBytes = SWAP ? 0 : kOutBufs * kStageOutBytes;    // output sub-tiles
   // in-kernel activation: codes (BN rows x 128 B, 128B swizzle) and one
   // 128-row scale block per K-step, for up to kActSteps steps
@@ -1055,6 +1057,8 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
             }
             return;
           }
+          // an empty bulk group: the wait in next_buf counts one a buffer
+          if (et == 0) bulk_commit_group();
           // 16-byte pieces of the rows that the group has.  (One at a time: four
           // in flight took registers from the slots that wait, and every tile
           // paid for it, 136 instead of 108 us for 64 ragged groups of 250 rows

@@ -155,7 +155,8 @@ def test_codes_past_4_gib():
 
 # ------------------------------------------------------------------ GEMM
 
-def run_gemm(rows, N, K, out_dtype, seed=0, T=None, **kw):
+def gemm_operands(rows, N, K, seed=0, T=None):
+    """Device operands of one grouped product, and its oracle result (computed when asked for)."""
     E, total = len(rows), sum(rows)
     T = max(1, total + 5) if T is None else T
     wc, ws, gw, host = experts(E, N, K, seed + 1)
@@ -163,12 +164,17 @@ def run_gemm(rows, N, K, out_dtype, seed=0, T=None, **kw):
     x = activation(max(1, total), K, seed + 2)
     codes, per = oracle_rows(x, rows, ga.numpy(), T, K)
     buf, _ = grouped_scales(per, T, K)
+    a = (torch.from_numpy(codes).cuda(), torch.from_numpy(buf).cuda(), ga.cuda(), wc, ws, gw, offsets_of(rows).cuda())
+    return a, T, lambda: product(codes, per, ga.numpy(), host, rows, N)
+
+
+def run_gemm(rows, N, K, out_dtype, seed=0, T=None):
+    a, T, ref = gemm_operands(rows, N, K, seed, T)
     out = torch.full((T, N), 777.0, dtype=out_dtype, device="cuda")
-    nv.nvfp4_grouped_gemm(torch.from_numpy(codes).cuda(), torch.from_numpy(buf).cuda(), ga.cuda(), wc, ws, gw,
-                          offsets_of(rows).cuda(), out, **kw)
+    nv.nvfp4_grouped_gemm(*a, out)
     torch.cuda.synchronize()
     check_device_error_word()
-    return out, lambda: product(codes, per, ga.numpy(), host, rows, N)
+    return out, ref
 
 
 @pytest.mark.parametrize("split", SPLITS)
@@ -199,6 +205,30 @@ def test_large_tiles_match_the_oracle(split, N, K):
     assert out[total:].eq(777.0).all()
     half, _ = run_gemm(rows, N, K, torch.bfloat16, T=T)
     assert torch.equal(half[:total], out[:total].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [[300, 48, 256, 100, 511, 64, 65, 31], [48, 100, 17, 128, 90, 64, 63, 1]])
+@pytest.mark.parametrize("K", [32, 96])
+def test_many_ragged_tiles_a_pair(rows, K, out_dtype):
+    """Short K and some tens of ragged tiles a CTA pair: every staging buffer is reused behind a TMA store and behind
+    masked stores, in every order."""
+    rows, N = rows * 5, 4608
+    a, T, ref = gemm_operands(rows, N, K)
+    want, first = ref(), None
+    for _ in range(5):
+        out = torch.full((T, N), 777.0, dtype=out_dtype, device="cuda")
+        nv.nvfp4_grouped_gemm(*a, out)
+        torch.cuda.synchronize()
+        check_device_error_word()
+        if first is None:
+            first = out
+            got = out[:sum(rows)].double().cpu().numpy()
+            if out_dtype == torch.float32:
+                assert_gemm_close(got, want)
+            tol = (2.0 ** -8 if out_dtype == torch.bfloat16 else 2.0 ** -20) * np.abs(want) + 1e-5 * np.abs(want).max()
+            assert np.all(np.abs(got - want) <= tol)
+        assert torch.equal(out, first)
 
 
 @pytest.mark.parametrize("E,N,K", [(512, 40, 64), (130, 136, 160)])
