@@ -54,7 +54,6 @@ constexpr int kSfChunk = 512;     // bytes of one 128-row x 4-scale chunk
 constexpr int kTmemCols = 512;
 constexpr int kGroupP = 64;       // tile raster: 64 P-tiles (8192 rows) share each Q-tile sweep
 constexpr int kStageOutBytes = 16384;   // one 128-row x 128-byte output sub-tile
-constexpr int kTileSlots = 16;    // grouped GEMM: ring of tile numbers
 constexpr int kEpiBar = 1;        // named barrier id of the 128 epilogue threads
 
 struct alignas(64) GemmParams {
@@ -126,7 +125,7 @@ struct GroupedGemmParams : GemmParams {
 // so a group's last tile costs what its rows cost, and each CTA loads its half
 // of them in the smallest of four boxes (16, 32, 64, 128 rows).  With the
 // activations on P, whose 256 rows are fixed, 32768 rows in 64 groups against
-// weights of 2048 x 5120 took 237 us instead of 219.  BN = 256 for large
+// weights of 2048 x 5120 took 8 % longer.  BN = 256 for large
 // groups; BN = 128 leaves room for more stages, and two whole accumulators.
 template <int BN, bool SWAP, int QX = 0, bool MX = false, bool PAIR = false, bool GROUPED = false>
 struct Cfg {
@@ -150,7 +149,7 @@ struct Cfg {
   static constexpr int kSfbBytes = kQx ? 0 : kSfbBlocks * kChunks * kSfChunk;
   static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
   // double-buffered; grouped tiles of BN = 128 give the second buffer to a
-  // seventh stage (72.6 against 73.7 us for 2 rows of each of 64 experts)
+  // seventh stage (1.5 % less time for 2 rows of each of 64 experts)
   static constexpr int kOutBufs = GROUPED && BN == 128 ? 1 : 2;
   // (Eight epilogue warps for grouped tiles of 256, on alternate tiles or on
   // alternate slots: 10 % less time at K = 512, 3 % more at K >= 2048.)
@@ -209,10 +208,7 @@ struct Cfg {
   static constexpr int kOffMisc = kOffSeg + 2 * 4 * NVFP4_MAX_SEGMENTS;
   static constexpr int kOffRtab = kOffMisc + 16;                     // in-kernel activation: g / e4m3(s)
   static constexpr int kOffTab = kOffRtab + (kQx ? 1024 : 0);        // grouped: table of groups
-  // grouped: the answer to a work request and its barrier, the ring of tile
-  // numbers and its barriers
-  static constexpr int kOffClc = (kOffTab + (GROUPED ? (int)sizeof(GroupTable) : 0) + 15) / 16 * 16;
-  static constexpr int kSmemBytes = kOffClc + (GROUPED ? 16 + 8 + kTileSlots * (8 + 4) : 0) + 1024;   // + alignment slack
+  static constexpr int kSmemBytes = kOffTab + (GROUPED ? (int)sizeof(GroupTable) : 0) + 1024;   // + alignment slack
   // TMEM columns.  Normal 128x256 tiles: the copy warps run ahead of the
   // MMAs, so the scales of successive steps use a ring of regions at the top
   // of TMEM ([320,512) for four 48-column regions); the two accumulator
@@ -322,79 +318,28 @@ __device__ __forceinline__ bool work_next(const GemmParams& p, WorkIter& w, int&
 // Work of a CTA pair of a grouped GEMM: tiles of 256 weight rows by up to BN
 // activation rows, numbered (group, weight tile, activation tile) with runs
 // of up to group_p activation tiles fastest, so that tiles in flight share
-// weights and activations in L2.  Groups leave tiles of every size, so they
-// are handed out as pairs get free: the grid has one cluster a tile (an upper
-// bound: the host does not know the offsets), and a running pair takes over
-// the clusters that have not started (cluster launch control), one ahead of
-// the tile it loads.  Dealt out in turn instead, 32768 rows in 64 groups left
-// the busiest pair 24 % above the mean; contiguous shares of equal cost are
-// balanced, but spread the pairs over all groups at once and their activations
-// over more than the L2 (325 us against 219).
-// The even CTA's loading thread asks for work and publishes each tile's number
-// (-1: the end) to every role of both CTAs through a ring of kTileSlots words
-// and barriers in either shared memory.  A slot is written again kTileSlots
-// tiles later; by then every role has read it: none can be more than the
-// pipeline's stages (each tile has a K step) and two accumulators behind the
-// loads.
+// weights and activations in L2.  The tiles are dealt out in turn, and every
+// role of either CTA counts through the same numbers.  That leaves the pairs
+// unequal (ragged groups have short tiles), but measured better than what
+// balances them: pairs that fetch the next tile when they get free (cluster
+// launch control) took 2-15 % longer (32768 rows in 64 groups against 2048 x
+// 5120: 218 us instead of 213; 16384 rows against 5120 x 1024: 87 instead of
+// 76), odd rounds dealt backwards the same to 9 % longer, and contiguous
+// shares of equal cost, which spread the pairs over all groups at once and
+// their activations over more than the L2, 325 us.
 struct GroupWork {
   const GroupTable* tab;
   int E, tiles_p, group_p;
   int total;                // tiles
-  int seq;                  // tiles published or read so far
-  int asked;                // requests made (issuer)
-  bool issuer;
-  bool ok;                  // no wait has run out
+  int round;
   int g, row0, rows, blk;   // current tile: group, first activation row, rows, first scale block
-  uint32_t ring;            // shared-memory addresses: tile numbers, their barriers, the answer, its barrier
-  uint32_t bars, answer, answer_bar;
-  volatile int* abort_flag;
-  unsigned* err;
-  uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ void group_publish(const GroupWork& w, int tile) {
-  const int slot = w.seq % kTileSlots;
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    st_cluster_u32(map_to_rank(w.ring + 4 * slot, r), (uint32_t)tile);
-    mbar_arrive_cluster(map_to_rank(w.bars + 8 * slot, r));
-  }
-}
-
-// Tile number of the next tile, -1 at the end (or when a wait ran out).
+// Number of the pair's next tile, -1 at the end.
 __device__ __forceinline__ int group_next_tile(GroupWork& w) {
-  int tile;
-  if (w.issuer) {
-    while (true) {
-      uint32_t first = blockIdx.x;
-      bool more = true;
-      if (w.asked > 0) {
-        if (!mbar_wait(w.answer_bar, (uint32_t)(w.asked - 1) & 1u, w.abort_flag, w.err, w.timeout_ns)) {
-          w.ok = false;
-          return -1;
-        }
-        more = clc_query(w.answer, first);
-        fence_proxy_async_smem();                           // read before the next asynchronous write
-      }
-      if (more) {
-        mbar_arrive_expect_tx(w.answer_bar, 16);
-        clc_try_cancel(w.answer, w.answer_bar);
-        ++w.asked;
-      }
-      tile = more ? (int)(first / 2) : -1;
-      if (tile < w.total) break;                            // the grid is an upper bound: go on to the next
-    }
-    group_publish(w, tile);
-  } else {
-    if (!mbar_wait_cluster(w.bars + 8 * (w.seq % kTileSlots), (uint32_t)(w.seq / kTileSlots) & 1u, w.abort_flag, w.err,
-                           w.timeout_ns)) {
-      w.ok = false;
-      return -1;
-    }
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(tile) : "r"(w.ring + 4 * (w.seq % kTileSlots)) : "memory");
-  }
-  ++w.seq;
-  return tile;
+  const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int tile = w.round++ * pairs + pair;
+  return tile < w.total ? tile : -1;
 }
 
 template <int BN>
@@ -512,8 +457,6 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     for (int s = 0; s < C::kStages; ++s) mbar_init(bar_sf + 8 * s, C::kCopyWarps);
     for (int i = 0; i < C::kCopyWarps; ++i) mbar_init(bar_cp_drain + 8 * i, 1);
     for (int j = 0; j < C::kActSteps; ++j) mbar_init(bar_act + 8 * j, 128);
-    if (GROUPED)
-      for (int s = 0; s <= kTileSlots; ++s) mbar_init(sbase + C::kOffClc + 16 + 8 * s, 1);
     *abort_flag = 0;
     fence_barrier_init();
     prefetch_tmap(&p.tmap_p);
@@ -552,7 +495,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     asm volatile("griddepcontrol.wait;" ::: "memory");
     load_groups<BN>(*reinterpret_cast<GroupTable*>(smem + C::kOffTab), p.offsets, p.E, p.M, p.err);
   }
-  auto begin_work = [&](bool issuer = false) {
+  auto begin_work = [&]() {
     if constexpr (GROUPED) {
       GroupWork w;
       w.tab = tab;
@@ -560,18 +503,8 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       w.tiles_p = p.tiles_p;
       w.group_p = p.group_p;
       w.total = tab->tiles[p.E] * p.tiles_p;
-      w.seq = 0;
-      w.issuer = issuer;
-      w.ok = true;
+      w.round = 0;
       w.g = w.row0 = w.rows = w.blk = 0;
-      w.asked = 0;
-      w.answer = sbase + C::kOffClc;
-      w.answer_bar = w.answer + 16;
-      w.bars = w.answer_bar + 8;
-      w.ring = w.bars + 8 * kTileSlots;
-      w.abort_flag = abort_flag;
-      w.err = p.err;
-      w.timeout_ns = p.timeout_ns;
       return w;
     } else {
       return work_begin(p, SWAP, PAIR);
@@ -601,10 +534,9 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       bool ok = true;
       // p0: this CTA's first row of P (CTA pairs: its 128-row half of the
       // 256-row tile); q0: the tile's first row of Q
-      auto for_steps = [&](auto&& w0, int first, int count, auto&& fn) {
+      auto for_steps = [&](const auto& w0, int first, int count, auto&& fn) {
         int tp, tq, kb, ke, j = 0;
-        // grouped: the walk asks for work as it goes, so there is only one
-        std::conditional_t<GROUPED, GroupWork&, WorkIter> w = w0;
+        auto w = w0;
         while (ok && j < first + count && next_work(w, tp, tq, kb, ke)) {
           TileSrc t;
           if constexpr (GROUPED) {
@@ -701,8 +633,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       if constexpr (GROUPED) {
         int stage = 0;
         uint32_t phase = 0;
-        auto w = begin_work(leader);
-        for_steps(w, 0, 1 << 30, [&](int, const TileSrc& t, int k) {
+        for_steps(begin_work(), 0, 1 << 30, [&](int, const TileSrc& t, int k) {
           if (!ok) return;
           if (!mbar_wait(bar_empty + 8 * stage, phase ^ 1, abort_flag, p.err, p.timeout_ns)) { ok = false; return; }
           expect(stage, t, k);
@@ -712,12 +643,6 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         });
-        // a request that is still out writes into this CTA: let it land (only
-        // a walk that gave up on a wait leaves one)
-        if (leader && !w.ok && w.asked > 0) {
-          volatile int never = 0;
-          (void)mbar_wait(w.answer_bar, (uint32_t)(w.asked - 1) & 1u, &never, p.err, p.drain_ns);
-        }
       } else {
         const auto w0 = begin_work();
         // prologue: the first kStages stages are free

@@ -50,7 +50,9 @@ struct GroupedQuantParams {
 // the encoding (some 140 instructions a block) is what it waits for: 2048 rows
 // of 5120 gathered 8 times take 31 us, and took 42 with a flat loop over blocks
 // (214 instructions each); 16384 rows once, 37 us (5.8 TB/s).
-constexpr int kQuantCtas = 3;   // CTAs an SM: all resident, one prologue each (4 of them: 33.1 against 31.4 us, 6 in two waves: 37)
+// Three CTAs an SM: all resident, with one prologue each (4 of them with fewer
+// registers took 33.1 us in the gathered case, 6 in two waves 37).
+constexpr int kQuantCtas = 3;
 
 template <bool kF32, bool kGlu>
 __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const GroupedQuantParams p) {
@@ -92,7 +94,7 @@ __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const
     const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + (have ? src : 0) * src_bytes + (int64_t)j0 * kB;
     uint2* codes = reinterpret_cast<uint2*>(p.codes) + (int64_t)row * p.nblk + j0;
     const uint32_t pos = (uint32_t)tab.blk[g] * 128u + (row - (uint32_t)tab.off[g]);
-    uint8_t* scales = p.scales + (int64_t)((pos >> 7) * p.kc) * 512 + (uint32_t)(j0 >> 5) * 4096u + lane_scale +
+    uint8_t* scales = p.scales + (int64_t)((pos >> 7) * p.kc) * 512 + (int64_t)(j0 >> 5) * 4096 + lane_scale +
                       (pos & 31) * 16 + ((pos >> 5) & 3) * 4;
     for (int j = j0; j < j_end; j += 32 * U) {
       Block16<kF32> B[U], C[kGlu ? U : 1];
@@ -143,8 +145,11 @@ __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const
 namespace {
 
 // Activation rows of a tile: 128 while groups are small (each CTA then keeps
-// 6 pipeline stages instead of 4 in flight, which is what streams weights),
-// 256 once they fill it.  The host knows only the mean rows of a group.
+// 7 pipeline stages instead of 4 in flight, which is what streams weights),
+// 256 once they fill it.  The host knows only the mean rows of a group.  Both
+// measured with 64 experts of 2048 x 5120, skewed groups: 8 rows a group on
+// average 70.4 (128) and 80.1 us (256), 64 rows 82.0 and 84.3, 128 rows 105.6
+// and 96.3, 187 rows 132 and 104.
 bool grouped_small(int64_t T, int64_t E) { return T < 128 * E; }
 
 template <int BN>
@@ -154,10 +159,10 @@ cudaError_t launch_grouped(GroupedGemmParams& p, const uint8_t* a_scales, const 
   if (!make_sf_map(&p.tmap_sfa, w_scales, w_blocks * 128, p.kc, C::kChunks) ||
       !make_sf_map(&p.tmap_sfb, a_scales, a_blocks * 128, p.kc, C::kChunks))
     return cudaErrorInvalidValue;
-  // one cluster for each tile there can be; running pairs take over those that have not started
+  // a pair of CTAs for each pair of SMs, but no more than there can be tiles
+  // (the host does not know the offsets)
   const int64_t tiles = (p.M + (BN - 1) * (p.E < p.M ? p.E : p.M)) / BN * p.tiles_p;
-  if (tiles > (1ll << 30) - 1) return cudaErrorInvalidValue;
-  const int grid = (int)tiles * 2;
+  const int grid = 2 * (int)(tiles < d->sm_count / 2 ? tiles : d->sm_count / 2);
   return f32 ? launch<BN, false, true, 0, false, true, true>(p, d, st, grid, 2)
              : launch<BN, false, false, 0, false, true, true>(p, d, st, grid, 2);
 }

@@ -63,7 +63,9 @@ __device__ __forceinline__ void load_groups(GroupTable& t, const int32_t* __rest
     if ((threadIdx.x & 31) == 0) out[E] = carry;
   };
   if (threadIdx.x < 32) prefix(t.blk, [](int r) { return (r + 127) >> 7; });
-  else if (kTileRows != 0 && threadIdx.x < 64) prefix(t.tiles, [](int r) { return kTileRows ? (r + kTileRows - 1) / (kTileRows ? kTileRows : 1) : 0; });
+  if constexpr (kTileRows != 0) {
+    if (threadIdx.x >= 32 && threadIdx.x < 64) prefix(t.tiles, [](int r) { return (r + kTileRows - 1) / kTileRows; });
+  }
   __syncthreads();
 }
 

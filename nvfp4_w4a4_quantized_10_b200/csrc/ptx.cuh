@@ -133,63 +133,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
-// mbar_wait whose success also orders what another CTA of the cluster wrote
-// before its release-arrival.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                                  unsigned* err, uint64_t timeout_ns) {
-  const uint64_t t0 = globaltimer_ns();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (*abort_flag) return false;
-    if (globaltimer_ns() - t0 > timeout_ns) {
-      atomicCAS(err, 0u, kErrTimeout);
-      *abort_flag = 1;
-      return false;
-    }
-  }
-}
-
-__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
-}
-
-// ---------------------------------------------------------------- cluster launch control
-// A running cluster takes over a cluster of its own grid that has not started
-// yet: the request cancels that launch, and its answer (16 bytes) arrives in
-// this CTA's shared memory, counted on mbarrier `bar`.  One thread of the
-// cluster asks.  No request may follow an answer that found nothing to cancel.
-__device__ __forceinline__ void clc_try_cancel(uint32_t answer, uint32_t bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                   answer),
-               "r"(bar)
-               : "memory");
-}
-
-// Whether the answer holds a cancelled cluster, and the x index of its first CTA.
-__device__ __forceinline__ bool clc_query(uint32_t answer, uint32_t& ctaid_x) {
-  uint32_t ok, x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
-      "ld.shared.b128 r, [%2];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t"
-      "mov.u32 %1, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
-      : "=r"(ok), "=r"(x)
-      : "r"(answer)
-      : "memory");
-  ctaid_x = x;
-  return ok != 0;
-}
-
 // ---------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* m) {
