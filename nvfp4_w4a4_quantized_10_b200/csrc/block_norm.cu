@@ -47,6 +47,7 @@ struct NormParams {
   int tc_layout;
   int64_t kc;
   uint64_t codes_bytes, scale_bytes, row_elems;
+  int ahead;               // one block a thread: a CTA fetches the rows of the one so far on into L2
   int wide;                // every row and weight starts on a 32-byte boundary
   unsigned* err;
 };
@@ -97,8 +98,6 @@ __device__ __forceinline__ float row_sum(float v, float* red, int warps) {
   return s;
 }
 
-__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 // NB: 16-element blocks of a thread; kWarpRow: a warp owns a row (K <= 512
 // NB), else a CTA does.  One row and done: the block scheduler then keeps
 // every SM's loads coming while other rows wait in their reductions (16384 x
@@ -122,10 +121,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
   const int nthr = kWarpRow ? 32 : blockDim.x;
   const int nblk = (int)(p.K / 16);
   constexpr int kB = kF32 ? 64 : 32;                             // bytes of a block
-  constexpr int kLine = 128 / kB;                                // blocks of a 128-byte line
-  // more than one block a thread: gate and residual are fetched into L2 and
-  // read where they are used, instead of being held in registers through the
-  // first norm
+  // more than one block a thread: gate and residual are read where they are
+  // used, instead of being held in registers through the first norm
   constexpr bool kHold = NB == 1;
   const float inv_k = 1.0f / (float)p.K;
   const bool wide = p.wide != 0;
@@ -146,15 +143,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
         if (j < nblk) load_block_wide<kF32>(block_at(p.gate, m, j), g, wide);
       }
     };
-    if constexpr (kHold) {
-      load_rest(0, R[0], G[0]);
-    } else {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const int j = t + b * nthr;
-        if (j >= nblk || j % kLine != 0) continue;
-        if (p.residual) prefetch_l2(block_at(p.residual, m, j));
-        if (kGate) prefetch_l2(block_at(p.gate, m, j));
+    if constexpr (kHold) load_rest(0, R[0], G[0]);
+    if constexpr (!kWarpRow) {
+      // whole rows, asked for by one thread, are in L2 sooner than by the
+      // loads of many: those of a later CTA, or, where the rows in flight and
+      // as many to come are more than L2 holds, this one's (4096 x 8192 bf16,
+      // residual and norm: 46.7 to 41.3 us; 2048 x 17408, gate and two norms:
+      // 84.0 to 79.7, and 99 with a later CTA's)
+      const int64_t at = kHold ? m + p.ahead : m;
+      if (threadIdx.x == 0 && at < p.M) {
+        const uint32_t bytes = (uint32_t)nblk * kB;
+        if (!kSlots) bulk_prefetch_l2(block_at(p.y, at, 0), bytes);
+        if (p.residual) bulk_prefetch_l2(block_at(p.residual, at, 0), bytes);
+        if constexpr (kGate) bulk_prefetch_l2(block_at(p.gate, at, 0), bytes);
       }
     }
     if constexpr (!kSlots) {
@@ -433,6 +434,7 @@ nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, in
   p.codes_bytes = (uint64_t)M * (uint64_t)(K / 2);
   p.scale_bytes = codes ? nvfp4_scale_bytes(M, K, layout) : 0;
   p.row_elems = (uint64_t)M * (uint64_t)K;
+  p.ahead = d->sm_count;
   p.wide = 1;
   for (const void* q : {y, (const void*)post_weight, gate, residual, (const void*)residual_out,
                         (const void*)pre_weight, (const void*)out})
