@@ -20,10 +20,13 @@
 #include "ptx.cuh"
 
 #include <initializer_list>
+#include <mutex>
 
 namespace nvfp4 {
 
 constexpr int kNormMaxK = 32768;
+// staged kernel: rows on their way to a CTA, of at least kRingRow bytes each
+constexpr int kRingRow = 64 * 1024, kRingBytes = 222 * 1024, kRingSlots = kRingBytes / kRingRow;
 
 struct NormParams {
   const void* y;
@@ -47,6 +50,8 @@ struct NormParams {
   int tc_layout;
   int64_t kc;
   uint64_t codes_bytes, scale_bytes, row_elems;
+  int ring_slots;          // staged kernel
+  uint64_t timeout_ns, drain_ns;
   int ahead;               // one block a thread: a CTA fetches the rows of the one so far on into L2
   int wide;                // every row and weight starts on a 32-byte boundary
   unsigned* err;
@@ -98,18 +103,86 @@ __device__ __forceinline__ float row_sum(float v, float* red, int warps) {
   return s;
 }
 
+// 16 elements from shared memory.  Threads read in turn the 16-byte pieces that
+// lie in different banks; selects put them in order.
+template <bool kF32>
+__device__ __forceinline__ void load_block_shared(uint32_t addr, Block16<kF32>& B) {
+  constexpr int kP = kF32 ? 4 : 2;
+  const int turn = (threadIdx.x >> (kF32 ? 1 : 2)) & (kP - 1);
+#pragma unroll
+  for (int i = 0; i < kP; ++i)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(B.v[i].x), "=r"(B.v[i].y), "=r"(B.v[i].z), "=r"(B.v[i].w)
+                 : "r"(addr + 16 * (i ^ turn))
+                 : "memory");
+#pragma unroll
+  for (int bit = 1; bit < kP; bit *= 2)
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      if (i & bit) continue;
+      const bool swap = turn & bit;
+      const uint4 lo = B.v[i], hi = B.v[i + bit];
+      B.v[i] = make_uint4(swap ? hi.x : lo.x, swap ? hi.y : lo.y, swap ? hi.z : lo.z, swap ? hi.w : lo.w);
+      B.v[i + bit] = make_uint4(swap ? lo.x : hi.x, swap ? lo.y : hi.y, swap ? lo.z : hi.z, swap ? lo.w : hi.w);
+    }
+}
+
+// Rows on their way through shared memory (staged kernel): a ring of slots of
+// one array's row each, filled by bulk copies in the order y, gate, residual,
+// next row's y, ...  A slot's barrier counts its copies; what has been read is
+// known from the barriers of the row's sums, after which thread 0 refills.
+struct RowRing {
+  uint32_t base, bars, bytes;
+  int slots, arrays;
+  int take_slot;
+  uint32_t take_phase;
+  int64_t put_row;           // next copy: row, array, slot
+  int put_array, put_slot, issued;
+};
+
+// Shared-memory address of the next array's row, once it is there.
+__device__ __forceinline__ uint32_t ring_take(RowRing& r, const NormParams& p, volatile int* abort_flag) {
+  // (a wait that runs out sets the error word; the rows are then not reliable)
+  (void)mbar_wait(r.bars + 8 * r.take_slot, r.take_phase, abort_flag, p.err, p.timeout_ns);
+  const uint32_t at = r.base + r.take_slot * r.bytes;
+  if (++r.take_slot == r.slots) {
+    r.take_slot = 0;
+    r.take_phase ^= 1;
+  }
+  return at;
+}
+
+__device__ __forceinline__ void ring_put(RowRing& r, const NormParams& p, volatile int* abort_flag) {
+  if (r.put_row >= p.M || *abort_flag) return;
+  const void* src = r.put_array == 0 ? p.y : r.put_array == 1 && p.gate ? p.gate : p.residual;
+  const uint32_t bar = r.bars + 8 * r.put_slot;
+  mbar_arrive_expect_tx(bar, r.bytes);
+  bulk_load(r.base + r.put_slot * r.bytes, reinterpret_cast<const uint8_t*>(src) + r.put_row * r.bytes, r.bytes, bar);
+  ++r.issued;
+  if (++r.put_slot == r.slots) r.put_slot = 0;
+  if (++r.put_array == r.arrays) {
+    r.put_array = 0;
+    r.put_row += gridDim.x;
+  }
+}
+
 // NB: 16-element blocks of a thread; kWarpRow: a warp owns a row (K <= 512
 // NB), else a CTA does.  One row and done: the block scheduler then keeps
 // every SM's loads coming while other rows wait in their reductions (16384 x
 // 5120 bf16, residual and norm: 121 us; a persistent grid of 2, 3, 4 or 6 CTAs
 // an SM that walks the rows: 143, 168, 129, 148).
+// kStaged: that persistent grid for the longest rows, one CTA an SM, with rows
+// on their way by bulk copies while others are computed (RowRing).
 // kThreads, kCtas: the CTA's most threads, and CTAs that are to fit on an SM
 // (which caps the registers; 48 of them instead of 56 are 4 CTAs instead of 3
 // and 99 instead of 108 us in that case).
-template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate, int kThreads, int kCtas>
+template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate, int kThreads, int kCtas, bool kStaged = false>
 __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormParams p) {
-  __shared__ float red[2][32];
+  __shared__ float red_s[kStaged ? 4 : 2][32];
   __shared__ float quot[8];
+  __shared__ uint64_t ring_bars[kStaged ? kRingSlots : 1];
+  __shared__ int abort_s;
+  extern __shared__ uint8_t ring_raw[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (p.codes) {                         // (uniform) seen by all after this barrier
@@ -126,16 +199,41 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
   constexpr bool kHold = NB == 1;
   const float inv_k = 1.0f / (float)p.K;
   const bool wide = p.wide != 0;
-  const int64_t m = kWarpRow ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
+  volatile int* abort_flag = &abort_s;
+  RowRing ring = {};
+  if constexpr (kStaged) {
+    ring.base = (smem_u32(ring_raw) + 127) & ~127u;
+    ring.bars = smem_u32(ring_bars);
+    ring.bytes = (uint32_t)nblk * kB;
+    ring.slots = p.ring_slots;
+    ring.arrays = 1 + (kGate ? 1 : 0) + (p.residual ? 1 : 0);
+    ring.put_row = blockIdx.x;
+    if (threadIdx.x == 0) {
+      abort_s = 0;
+      for (int i = 0; i < ring.slots; ++i) mbar_init(ring.bars + 8 * i, 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int i = 0; i < ring.slots; ++i) ring_put(ring, p, abort_flag);
+  }
   auto block_at = [&](const void* base, int64_t row, int j) {
     return reinterpret_cast<const uint8_t*>(base) + (row * nblk + j) * kB;
   };
-  if (m < p.M) {
+  auto do_row = [&](const int64_t m, float (*red)[32]) {
     float f[NB][16];
+    int unread = kStaged ? ring.arrays : 0;              // arrays of this row that have not been given back
+    uint32_t ring_gate = 0, ring_res = 0;
     // ------------------------------------------------ branch
     Block16<kF32> R[kHold ? NB : 1], G[kHold && kGate ? NB : 1];
     auto load_rest = [&](int b, Block16<kF32>& r, Block16<kF32>& g) {
       const int j = t + b * nthr;
+      if constexpr (kStaged) {
+        r = g = Block16<kF32>{};
+        if (j < nblk && p.residual) load_block_shared<kF32>(ring_res + j * kB, r);
+        if (kGate && j < nblk) load_block_shared<kF32>(ring_gate + j * kB, g);
+        return;
+      }
       r = Block16<kF32>{};
       if (j < nblk && p.residual) load_block_wide<kF32>(block_at(p.residual, m, j), r, wide);
       if constexpr (kGate) {
@@ -144,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
       }
     };
     if constexpr (kHold) load_rest(0, R[0], G[0]);
-    if constexpr (!kWarpRow) {
+    if constexpr (!kWarpRow && !kStaged) {
       // whole rows, asked for by one thread, are in L2 sooner than by the
       // loads of many: those of a later CTA, or, where the rows in flight and
       // as many to come are more than L2 holds, this one's (4096 x 8192 bf16,
@@ -160,11 +258,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
     }
     if constexpr (!kSlots) {
       Block16<kF32> B[NB];
+      uint32_t ring_y = 0;
+      if constexpr (kStaged) ring_y = ring_take(ring, p, abort_flag);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int j = t + b * nthr;
         B[b] = Block16<kF32>{};
-        if (j < nblk) load_block_wide<kF32>(block_at(p.y, m, j), B[b], wide);
+        if (kStaged && j < nblk) load_block_shared<kF32>(ring_y + j * kB, B[b]);
+        if (!kStaged && j < nblk) load_block_wide<kF32>(block_at(p.y, m, j), B[b], wide);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) block_floats<kF32>(B[b], f[b]);
@@ -226,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
 #pragma unroll
         for (int b = 0; b < NB; ++b) s += ss[b];
         s = row_sum<kWarpRow>(s, red[0], warps);
+        if (kStaged) {                                   // every thread has read y
+          if (threadIdx.x == 0) ring_put(ring, p, abort_flag);
+          --unread;
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b) ss[b] = s;
       } else {
@@ -249,6 +354,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
     }
     // ------------------------------------------------ gate, residual stream
     float s = 0.0f;
+    if constexpr (kStaged) {
+      if (kGate) ring_gate = ring_take(ring, p, abort_flag);
+      if (p.residual) ring_res = ring_take(ring, p, abort_flag);
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int j = t + b * nthr;
@@ -280,8 +389,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
         store_block<kF32>(const_cast<uint8_t*>(block_at(p.residual_out, m, j)), f[b], wide);
     }
     // ------------------------------------------------ norm before the next block
+    if (p.pre_weight) s = row_sum<kWarpRow>(s, red[1], warps);
+    else if (kStaged) __syncthreads();
+    if (kStaged && threadIdx.x == 0)                     // every thread has read the row
+      for (; unread > 0; --unread) ring_put(ring, p, abort_flag);
     if (p.pre_weight) {
-      s = row_sum<kWarpRow>(s, red[1], warps);
       const float r = rsqrtf(fmaf(s, inv_k, p.eps));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -321,6 +433,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
         }
       }
     }
+  };
+  if constexpr (kStaged) {
+    // (a row's sums lie in slots that the next row's do not use)
+    int turn = 0;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x, turn ^= 2) do_row(m, red_s + turn);
+    // after a wait that ran out, copies may still be on their way
+    if (threadIdx.x == 0 && *abort_flag) {
+      volatile int never = 0;
+      for (int i = 0; i < ring.slots && i < ring.issued; ++i)
+        (void)mbar_wait(ring.bars + 8 * i, (uint32_t)((ring.issued - 1 - i) / ring.slots) & 1u, &never, p.err,
+                        p.drain_ns);
+    }
+  } else {
+    const int64_t m = kWarpRow ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
+    if (m < p.M) do_row(m, red_s);
   }
   // padding rows of the tensor-core layout (up to 127 past M): zero scales,
   // one row a CTA
@@ -349,11 +476,31 @@ cudaError_t launch_norm_as(const NormParams& p, int grid, int threads, cudaStrea
              : launch_pdl(block_norm_kernel<kF32, NB, kWarpRow, false, false, kThreads, kCtas>, grid, threads, st, p);
 }
 
+// Staged kernel: one CTA an SM.
+template <bool kF32, int NB, int kThreads>
+cudaError_t launch_norm_staged(NormParams& p, const DeviceInfo* d, int threads, cudaStream_t st) {
+  auto run = [&](auto kern, std::once_flag& once, cudaError_t& attr) {
+    std::call_once(once, [&] {
+      attr = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes + 128);
+    });
+    if (attr != cudaSuccess) return attr;
+    const int64_t row = p.K * (kF32 ? 4 : 2);
+    p.ring_slots = (int)(kRingBytes / row);
+    return launch_pdl_smem(kern, d->sm_count, threads, p.ring_slots * row + 128, st, p);
+  };
+  static std::once_flag once[2][64];
+  static cudaError_t attr[2][64];
+  return p.gate ? run(block_norm_kernel<kF32, NB, false, false, true, kThreads, 1, true>, once[1][d->device],
+                      attr[1][d->device])
+                : run(block_norm_kernel<kF32, NB, false, false, false, kThreads, 1, true>, once[0][d->device],
+                      attr[0][d->device]);
+}
+
 // Rows of at most 1024 elements: a warp each, 8 to a CTA.  Longer ones: a CTA
 // each, with one 16-element block a thread while registers allow (K up to
 // 8192), then two (18432), then four.
 template <bool kF32>
-cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
+cudaError_t launch_norm(NormParams& p, const DeviceInfo* d, cudaStream_t st) {
   const int nblk = (int)(p.K / 16);
   const int64_t padding = p.codes && p.tc_layout ? ceil_div(p.M, 128) * 128 - p.M : 0;
   auto ctas = [&](int64_t rows) { return (int)(rows > padding ? rows : padding); };
@@ -366,6 +513,19 @@ cudaError_t launch_norm(const NormParams& p, cudaStream_t st) {
   auto threads = [&](int nb) { return (int)ceil_div(ceil_div(nblk, nb), 32) * 32; };
   if (nblk <= 320) return launch_norm_as<kF32, 1, false, 320, 4>(p, grid, threads(1), st);
   if (nblk <= 512) return launch_norm_as<kF32, 1, false, 512, 2>(p, grid, threads(1), st);
+  // Staged: rows of at least 64 KB without slots whose inputs fit in the ring,
+  // and more than two of them an SM.  In 4 bytes, 1003 x 17408, gate, residual
+  // and two norms: 69.8 us, not staged 80.5 (150 rows: 21.0 and 20.1); 2048 x
+  // 16384: 117 and 138; 2048 x 20480, residual and norm: 109 and 116; in 2
+  // bytes, 1024 x 32768: 50.6 and 56.3, with gate and two norms 91.0 and 89.9.
+  // On shorter rows the one CTA's instructions show: 2048 x 10240 in 4 bytes,
+  // gate and two norms 93.2 and 86.1, 2048 x 17408 in 2 bytes 101 and 79.7.
+  const int64_t row = p.K * (kF32 ? 4 : 2), inputs = (1 + (p.gate != nullptr) + (p.residual != nullptr)) * row;
+  if (!p.slots && p.M > 2 * d->sm_count && row >= kRingRow && inputs <= kRingBytes) {
+    if constexpr (kF32)                            // (in 2 bytes only longer rows have 64 KB)
+      if (nblk <= 2 * 576) return launch_norm_staged<kF32, 2, 576>(p, d, threads(2), st);
+    return launch_norm_staged<kF32, 4, 512>(p, d, threads(4), st);
+  }
   if (nblk <= 2 * 576) return launch_norm_as<kF32, 2, false, 576, 2>(p, grid, threads(2), st);
   return launch_norm_as<kF32, 4, false, 512, 1>(p, grid, threads(4), st);
 }
@@ -435,13 +595,15 @@ nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, in
   p.scale_bytes = codes ? nvfp4_scale_bytes(M, K, layout) : 0;
   p.row_elems = (uint64_t)M * (uint64_t)K;
   p.ahead = d->sm_count;
+  p.timeout_ns = wait_timeout_ns();
+  p.drain_ns = drain_timeout_ns();
   p.wide = 1;
   for (const void* q : {y, (const void*)post_weight, gate, residual, (const void*)residual_out,
                         (const void*)pre_weight, (const void*)out})
     if (reinterpret_cast<uintptr_t>(q) & 31) p.wide = 0;
   p.err = d->err_word;
   cudaStream_t st = (cudaStream_t)stream;
-  return cuda_status(dtype == NVFP4_IN_F32 ? launch_norm<true>(p, st) : launch_norm<false>(p, st));
+  return cuda_status(dtype == NVFP4_IN_F32 ? launch_norm<true>(p, d, st) : launch_norm<false>(p, d, st));
 }
 
 }  // extern "C"

@@ -63,10 +63,11 @@ inline nvfp4_status cuda_status(cudaError_t e) {
 // the kernel may start while that one finishes, and waits
 // (griddepcontrol.wait) before it touches memory.
 template <typename Kernel, typename... A>
-inline cudaError_t launch_pdl(Kernel kern, int grid, int threads, cudaStream_t st, A... args) {
+inline cudaError_t launch_pdl_smem(Kernel kern, int grid, int threads, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -74,6 +75,11 @@ inline cudaError_t launch_pdl(Kernel kern, int grid, int threads, cudaStream_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename Kernel, typename... A>
+inline cudaError_t launch_pdl(Kernel kern, int grid, int threads, cudaStream_t st, A... args) {
+  return launch_pdl_smem(kern, grid, threads, 0, st, args...);
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

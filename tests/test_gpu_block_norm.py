@@ -131,6 +131,52 @@ def test_sandwich_with_gate(M, K, dtype, gate):
     check(make(M, K, dtype, post=K, gate=gate), dtype, layout=nv.SF_ROWMAJOR)
 
 
+# long rows, more than two an SM: staged through shared memory, several to a CTA, in rings of 1 to 3 rows
+@pytest.mark.parametrize("M,K", [(297, 16384), (460, 17408), (300, 18464), (300, 18944), (300, 32768)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_long_rows(M, K, dtype):
+    check(make(M, K, dtype, post=K, gate=nv.GATE_SILU), dtype)
+
+
+@pytest.mark.parametrize("M,K,over", [(600, 16384, dict()), (460, 16416, dict(residual=False)),
+                                      (460, 16384, dict(post=512, gate=nv.GATE_SILU, residual=False, pre=False)),
+                                      (460, 17408, dict(post=256)), (460, 18944, dict(residual=False, pre=False)),
+                                      (300, 24576, dict(post=24576, pre=False, gate=nv.GATE_LINEAR, residual=False)),
+                                      (300, 32768, dict(post=32768, residual=False)), (330, 32768, dict(pre=False))])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_long_rows_with_fewer_inputs(M, K, over, dtype):
+    check(make(M, K, dtype, **over), dtype, layout=nv.SF_ROWMAJOR)
+
+
+@pytest.mark.parametrize("K", [5120, 17408])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_a_row_does_not_depend_on_how_many_there_are(K, dtype):
+    a = make(310, K, dtype, post=K, gate=nv.GATE_SIGMOID)
+    out, few = (torch.empty(310, K, dtype=dtype, device="cuda") for _ in range(2))
+    nv.nvfp4_block_norm(**a, out=out)
+    for i in range(0, 310, 31):
+        part = {n: t[i:i + 31] if torch.is_tensor(t) and t.dim() == 2 else t for n, t in a.items()}
+        nv.nvfp4_block_norm(**part, out=few[i:i + 31])
+    assert torch.equal(out, few)
+    torch.cuda.synchronize()
+    check_device_error_word()
+
+
+@pytest.mark.parametrize("into", ["residual", "gate", "y"])
+def test_many_long_rows_in_place(into):
+    M, K = 320, 17408
+    a = make(M, K, torch.float32, post=K, gate=nv.GATE_SILU)
+    want_r, want = torch.empty(M, K, device="cuda"), torch.empty(M, K, device="cuda")
+    nv.nvfp4_block_norm(**a, residual_out=want_r, out=want)
+    other = torch.empty(M, K, device="cuda")
+    b = {n: t.clone() if torch.is_tensor(t) else t for n, t in a.items()}
+    nv.nvfp4_block_norm(**b, residual_out=b[into], out=other)
+    assert torch.equal(b[into], want_r) and torch.equal(other, want)
+    b = {n: t.clone() if torch.is_tensor(t) else t for n, t in a.items()}
+    nv.nvfp4_block_norm(**b, residual_out=other, out=b[into])
+    assert torch.equal(other, want_r) and torch.equal(b[into], want)
+
+
 @pytest.mark.parametrize("K,width", [(32, 16), (64, 32), (512, 64), (768, 256), (1024, 512), (4096, 128), (5120, 256),
                                      (8704, 512), (512, 512)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
