@@ -284,3 +284,22 @@ def test_more_than_2_31_elements():
     nv.nvfp4_block_norm(y, pre_weight=w, out=y)
     assert torch.equal(y[at], small)
     assert y[2].eq(0).all() and y[M - 2].eq(0).all()
+
+
+def test_staged_rows_survive_a_wait_that_runs_out():
+    M, K = 320, 17408
+    a = make(M, K, torch.float32, post=K, gate=nv.GATE_SILU)
+    want, out = torch.empty(M, K, device="cuda"), torch.empty(M, K, device="cuda")
+    nv.nvfp4_block_norm(**a, out=want)
+    torch.cuda.synchronize()
+    try:
+        nv.nvfp4_set_wait_timeout_ns(1)
+        nv.nvfp4_block_norm(**a, out=out)
+        # (a copy may have landed at the first look)
+        assert nv.nvfp4_last_device_error() in (nv.OK, nv.ERR_TIMEOUT)
+    finally:
+        nv.nvfp4_set_wait_timeout_ns(0)
+    nv.nvfp4_block_norm(**a, out=out)
+    torch.cuda.synchronize()
+    check_device_error_word()
+    assert torch.equal(out, want)
