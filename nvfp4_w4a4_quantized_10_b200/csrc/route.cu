@@ -9,7 +9,7 @@
 //
 // The bytes (logits once, 16 a pair) take a microsecond at any size met in
 // serving; what both kernels wait for is instructions and latency (8 tokens
-// of 64 experts 3.5 us; 16384 of 128, top 8, 15.7 us, some 550 warp
+// of 64 experts 3.4 us; 16384 of 128, top 8, 16.3 us, some 550 warp
 // instructions a token in the first kernel).
 //
 // Selection: one warp a token, each lane holding E / 32 logits as ordered
@@ -20,7 +20,8 @@
 // expert (an OR is order-free, so the result does not depend on timing), and
 // a pair's rank is the number of bits below its own.  Each CTA counts a
 // contiguous run of tokens; the second kernel adds up the runs before it.  A
-// call with few tokens runs as one CTA of one launch.
+// call with few tokens is one launch of one cluster, whose CTAs read one
+// another's counts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -37,6 +38,7 @@ constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kSub = 128;               // tokens ranked at a time
 constexpr int kMaxTopK = NVFP4_MAX_TOP_K;
 constexpr int kRouteMaxChunks = 256;
+constexpr int kRouteCluster = 8;        // CTAs of a call that is one launch
 
 struct RouteParams {
   const void* logits;
@@ -89,6 +91,12 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
 // Experts in a row of the counts of all runs: rows start on 16 bytes.
 __host__ __device__ constexpr int hist_stride(int E) { return (E + 3) & ~3; }
 
+__device__ __forceinline__ int ld_cluster(const int* p, int rank) {
+  int v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(map_to_rank(smem_u32(p), rank)) : "memory");
+  return v;
+}
+
 // By one warp: v[e] becomes the sum of v[0 .. e - 1]; returns the total.
 __device__ __forceinline__ int warp_exclusive(int* v, int E) {
   const int lane = threadIdx.x & 31;
@@ -107,11 +115,18 @@ __device__ __forceinline__ int warp_exclusive(int* v, int E) {
   return carry;
 }
 
-template <bool kF32, int NV>
+// kOne: the grid is one cluster, each CTA has at most kSub tokens, and ranks
+// become slots here.  Else they are ranks inside the CTA's run.
+// Registers for one CTA an SM: with room for two, grids smaller than the
+// machine are doubled up on some SMs (8192 tokens of 128 experts 15.1 us
+// instead of 11.1; 16384, a run on every SM, 15.2 instead of 16.3).
+template <bool kF32, int NV, bool kOne>
 __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RouteParams p) {
   __shared__ uint32_t mask[kMaxGroups][kSub / 32];
   __shared__ int count[kMaxGroups];
   __shared__ int16_t ids_s[kSub * kMaxTopK];
+  __shared__ int16_t rank_s[kOne ? kSub * kMaxTopK : 1];
+  __shared__ int all[kOne ? kMaxGroups : 1], before[kOne ? kMaxGroups : 1];
   __shared__ int total_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = p.E, k = p.k;
@@ -199,7 +214,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
           rank += __popc(mask[e][w] & below);
         }
       }
-      p.slots[sub * k + i] = rank;               // rank inside this run of tokens
+      if constexpr (kOne) rank_s[i] = (int16_t)rank;
+      else p.slots[sub * k + i] = rank;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kRouteThreads) {
@@ -210,28 +226,43 @@ __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RoutePa
     }
     __syncthreads();
   }
-  if (gridDim.x > 1) {
+  if constexpr (!kOne) {
     for (int e = threadIdx.x; e < E; e += kRouteThreads) p.hist[(int64_t)blockIdx.x * hist_stride(E) + e] = count[e];
     return;
   }
-  // the only CTA: ranks become slots here
+  const int ctas = gridDim.x, rank = blockIdx.x;
+  int* start = count;                            // becomes each expert's first slot
+  if (ctas > 1) {
+    start = all;
+    cluster_sync();                              // every CTA has its counts
+    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+      int sum = 0, head = 0;
+      for (int c = 0; c < ctas; ++c) {
+        const int v = c == rank ? count[e] : ld_cluster(&count[e], c);
+        sum += v;
+        if (c < rank) head += v;
+      }
+      all[e] = sum;
+      before[e] = head;
+    }
+    __syncthreads();
+  }
   if (warp == 0) {
-    const int t = warp_exclusive(count, E);
+    const int t = warp_exclusive(start, E);
     if (lane == 0) total_s = t;
   }
   __syncthreads();
   const int total = total_s;
-  for (int e = threadIdx.x; e <= E; e += kRouteThreads) p.offsets[e] = e < E ? count[e] : total;
-  const int pairs = (int)(p.M * k);
+  if (rank == 0)
+    for (int e = threadIdx.x; e <= E; e += kRouteThreads) p.offsets[e] = e < E ? start[e] : total;
+  const int first = (int)(m_begin * k), pairs = m_begin < m_end ? (int)(m_end - m_begin) * k : 0;
   for (int i = threadIdx.x; i < pairs; i += kRouteThreads) {
-    const int e = p.ids[i];
-    if (e >= 0) {
-      const int s = count[e] + p.slots[i];
-      p.slots[i] = s;
-      p.row_index[s] = i / k;
-    }
-    if (i >= total) p.row_index[i] = -1;
+    const int e = ids_s[i], slot = e >= 0 ? start[e] + (ctas > 1 ? before[e] : 0) + rank_s[i] : -1;
+    p.slots[first + i] = slot;
+    if (e >= 0) p.row_index[slot] = (first + i) / k;
+    if (first + i >= total) p.row_index[first + i] = -1;
   }
+  if (ctas > 1) cluster_sync();                  // no CTA leaves while its counts may be read
 }
 
 // Second launch of a call with more than one run of tokens: every CTA adds up
@@ -308,24 +339,49 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
 
 namespace {
 
-// Runs of tokens: one CTA and one launch up to 32 tokens, one a warp (64
-// tokens that way took 7.9 us; as two runs and two launches 128 take 7.1), else
-// at least 32 tokens a run, one for each warp, and at most one run an SM.
+// Runs of tokens: at least 32 tokens a run, one for each warp, and at most one
+// run an SM.  One launch while a cluster has a warp for each token: 256 tokens
+// of 128 experts 6.6 us, in two launches 7.1 (33 tokens 5.5 and 6.2); with more
+// tokens a warp it is slower (512: 9.4 and 7.1).
 int64_t route_chunks(int64_t M, int sms) {
-  if (M <= kRouteWarps) return 1;
+  int64_t c = ceil_div(M, kRouteWarps);
+  if (M <= kRouteCluster * kRouteWarps) {
+    c = c < kRouteCluster ? c : kRouteCluster;
+    while (c & (c - 1)) ++c;                     // a cluster of 1, 2, 4 or 8; no CTA without tokens
+    return c;
+  }
   const int64_t cap = sms < kRouteMaxChunks ? sms : kRouteMaxChunks;
-  const int64_t c = ceil_div(M, kRouteWarps);
   return c < cap ? c : cap;
 }
 
-template <bool kF32>
+template <bool kF32, bool kOne>
 cudaError_t launch_topk(const RouteParams& p, int grid, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kRouteThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)grid;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kOne && grid > 1 ? 2 : 1;
   const int nv = (p.E + 31) / 32;
-  if (nv <= 1) return launch_pdl(route_topk_kernel<kF32, 1>, grid, kRouteThreads, st, p);
-  if (nv <= 2) return launch_pdl(route_topk_kernel<kF32, 2>, grid, kRouteThreads, st, p);
-  if (nv <= 4) return launch_pdl(route_topk_kernel<kF32, 4>, grid, kRouteThreads, st, p);
-  if (nv <= 8) return launch_pdl(route_topk_kernel<kF32, 8>, grid, kRouteThreads, st, p);
-  return launch_pdl(route_topk_kernel<kF32, 16>, grid, kRouteThreads, st, p);
+  if (nv <= 1) return cudaLaunchKernelEx(&cfg, route_topk_kernel<kF32, 1, kOne>, p);
+  if (nv <= 2) return cudaLaunchKernelEx(&cfg, route_topk_kernel<kF32, 2, kOne>, p);
+  if (nv <= 4) return cudaLaunchKernelEx(&cfg, route_topk_kernel<kF32, 4, kOne>, p);
+  if (nv <= 8) return cudaLaunchKernelEx(&cfg, route_topk_kernel<kF32, 8, kOne>, p);
+  return cudaLaunchKernelEx(&cfg, route_topk_kernel<kF32, 16, kOne>, p);
+}
+
+template <bool kF32>
+cudaError_t launch_route(const RouteParams& p, int grid, cudaStream_t st) {
+  if (grid <= kRouteCluster && p.chunk <= kSub) return launch_topk<kF32, true>(p, grid, st);
+  const cudaError_t e = launch_topk<kF32, false>(p, grid, st);
+  return e == cudaSuccess ? launch_pdl(route_slots_kernel, grid, kRouteThreads, st, p) : e;
 }
 
 }  // namespace
@@ -373,9 +429,7 @@ nvfp4_status nvfp4_route(const void* logits, nvfp4_in_dtype dtype, int64_t M, in
   p.chunk = ceil_div(M, route_chunks(M, d->sm_count));
   const int grid = (int)ceil_div(M, p.chunk);
   cudaStream_t st = (cudaStream_t)stream;
-  cudaError_t e = dtype == NVFP4_IN_F32 ? launch_topk<true>(p, grid, st) : launch_topk<false>(p, grid, st);
-  if (e == cudaSuccess && grid > 1) e = launch_pdl(route_slots_kernel, grid, kRouteThreads, st, p);
-  return cuda_status(e);
+  return cuda_status(dtype == NVFP4_IN_F32 ? launch_route<true>(p, grid, st) : launch_route<false>(p, grid, st));
 }
 
 }  // extern "C"

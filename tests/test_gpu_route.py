@@ -130,3 +130,13 @@ def test_captured_and_replayed_on_new_logits():
         assert np.array_equal(b["slots"].cpu().numpy(), slots)
         assert np.array_equal(b["row_index"].cpu().numpy(), rows)
         assert np.array_equal(b["group_offsets"].cpu().numpy(), offsets)
+
+
+# one launch: a CTA up to 32 tokens, then a cluster of 2, 4 or 8; two launches beyond
+@pytest.mark.parametrize("M", [31, 32, 33, 63, 64, 65, 96, 127, 128, 129, 160, 255, 256, 257, 511, 512, 513, 1023, 1024,
+                               1025])
+@pytest.mark.parametrize("E,k,dtype", [(60, 3, torch.float32), (512, 32, torch.bfloat16)])
+def test_every_number_of_runs(M, E, k, dtype):
+    x = torch.randn(M, E, generator=torch.Generator().manual_seed(M))
+    x[M // 2:, E // 3:] = float("-inf")                   # tokens with fewer than k experts
+    check(x.to(dtype).cuda(), k, nv.ROUTE_SOFTMAX_ALL)
