@@ -434,6 +434,8 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
   float* seg_alpha_s = reinterpret_cast<float*>(smem + C::kOffSeg + 4 * NVFP4_MAX_SEGMENTS);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* epi_stop = abort_flag + 1;       // epilogue: the tile whose wait ran out
+  constexpr int kNoTile = 0x7FFFFFFF;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -458,6 +460,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     for (int i = 0; i < C::kCopyWarps; ++i) mbar_init(bar_cp_drain + 8 * i, 1);
     for (int j = 0; j < C::kActSteps; ++j) mbar_init(bar_act + 8 * j, 128);
     *abort_flag = 0;
+    *epi_stop = kNoTile;
     fence_barrier_init();
     prefetch_tmap(&p.tmap_p);
     prefetch_tmap(&p.tmap_q);
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     int tp, tq, kb0, ke0;
     // CTA pairs: only the even CTA issues (for both)
     while (ok && leader && next_work(w, tp, tq, kb0, ke0)) {
-      if (!mbar_wait(bar_acc_empty, acc_phase ^ 1, abort_flag, p.err, p.timeout_ns)) break;
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar_acc_empty, acc_phase ^ 1, abort_flag, p.err, p.timeout_ns))) break;
       tc_fence_after();
       uint32_t idesc = idesc_full;
       // as many columns as the tile has rows; each CTA of a pair holds half
@@ -754,9 +757,9 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
           ok = false;
           break;
         }
-        if (!mbar_wait(bar_sf + 8 * stage, phase, abort_flag, p.err, p.timeout_ns)) { ok = false; break; }
+        const bool there = mbar_wait(bar_sf + 8 * stage, phase, abort_flag, p.err, p.timeout_ns);
         tc_fence_after();
-        if (lane == 0) {
+        if (lane == 0 && there) {
           const uint32_t sfa_t = sf_t0 + region * C::kSfStageCols;
           const uint32_t sfb_t = sfa_t + C::kSfaCols;
           const uint64_t ad = a_desc0 + (uint64_t)((stage * C::kABytes) >> 4);
@@ -788,7 +791,8 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
           if constexpr (PAIR) tc_commit_pair_both(bar_empty + 8 * stage);
           else tc_commit(bar_empty + 8 * stage);
         }
-        __syncwarp();
+        ok = __all_sync(0xFFFFFFFFu, there);     // the lanes stop together
+        if (!ok) break;
         if (++stage == C::kStages) { stage = 0; phase ^= 1; }
         if (++region == C::kSfRegions) region = 0;
         ++lstep;
@@ -822,6 +826,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
     const bool tma_store = !SWAP && p.tma_store;
     uint32_t acc_phase = 0, acc_buf = 0;
     uint32_t out_buf = 0;                    // next staging buffer (TMA store path)
+    int tile_no = 0;                         // tiles of this CTA so far
     auto w = begin_work();
     const int64_t U = (int64_t)p.tiles_p * p.kt, G = gridDim.x;
     int tp, tq, kb0, ke0;
@@ -938,8 +943,22 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       if constexpr (GROUPED) {
         g_alpha = (float)(1.0 / ((double)__ldg(p.ga + w.g) * (double)__ldg(p.gw + w.g)));
       }
-      if (!mbar_wait(bar_acc_full, acc_phase, abort_flag, p.err, p.timeout_ns)) break;
-      __syncwarp();
+      // A warp goes on as a whole or not at all.  Where the four warps share
+      // staging buffers they also stop together, at the end of the first tile
+      // for which a wait ran out in any of them: that warp writes the tile's
+      // number before the tile's first barrier and goes through its barriers
+      // with the others (what the tile stores is then not reliable), and
+      // behind the last of them all read that number, or a later one, which
+      // is not for this tile.  (Nothing on the way of a tile: agreeing by a
+      // barrier before the TMEM loads took 107 instead of 101 us for 16000
+      // rows in 64 groups against 5120 x 1024, making each store depend on
+      // the number 123 instead of 114 for FP32 against 4096 x 256.)
+      const bool there = __all_sync(0xFFFFFFFFu, mbar_wait(bar_acc_full, acc_phase, abort_flag, p.err, p.timeout_ns));
+      ++tile_no;
+      if (!there) {
+        if (!(GROUPED || tma_store)) break;
+        *epi_stop = tile_no;
+      }
       tc_fence_after();
       if constexpr (GROUPED && PAIR) {
         // Lane = weight row = output column n, accumulator column = activation
@@ -1354,6 +1373,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
           }
         }
       }
+      if ((GROUPED || tma_store) && *epi_stop <= tile_no) break;
       acc_phase ^= 1;
       acc_buf ^= 1;
       first_item = false;

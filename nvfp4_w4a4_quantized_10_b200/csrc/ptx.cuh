@@ -87,7 +87,10 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 
 // Wait until the phase with the given parity has completed.  Returns false if
 // the CTA is aborting or the wait exceeded timeout_ns (then the error word is
-// set and the abort flag raised).
+// set and the abort flag raised).  Each thread decides for itself: where a
+// barrier completes just as a wait on it gives up, some threads of a warp get
+// true and others false.  Code that threads only run together (.aligned
+// instructions, warp and named barriers) first agrees on one verdict.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           unsigned* err, uint64_t timeout_ns) {
   if (mbar_try_wait(bar, parity)) return true;
