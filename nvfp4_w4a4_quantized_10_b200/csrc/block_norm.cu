@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
 #pragma unroll
         for (int c = 0; c < kCh; ++c) {
           const int64_t at = m * p.top_k + q0 + c;
-          src[c] = q0 + c < p.top_k ? __ldg(p.slots + at) : -1;
-          w[c] = q0 + c < p.top_k ? __ldg(p.slot_weights + at) : 0.0f;
+          src[c] = q0 + c < p.top_k ? p.slots[at] : -1;
+          w[c] = q0 + c < p.top_k ? p.slot_weights[at] : 0.0f;
         }
         Block16<kF32> B[kCh][NB];
 #pragma unroll

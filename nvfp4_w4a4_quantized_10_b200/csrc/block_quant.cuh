@@ -92,13 +92,12 @@ struct Block16 {
   uint4 v[kF32 ? 4 : 2];
 };
 
-// The 16 elements at p (16-byte aligned), through the L1/L2 read-only path
-// (for data that several CTAs read).
+// The 16 elements at p (16-byte aligned), for data that several CTAs read.
 template <bool kF32>
 __device__ __forceinline__ void load_block_at(const void* p, Block16<kF32>& B) {
   const uint4* q = reinterpret_cast<const uint4*>(p);
 #pragma unroll
-  for (int i = 0; i < (kF32 ? 4 : 2); ++i) B.v[i] = __ldg(q + i);
+  for (int i = 0; i < (kF32 ? 4 : 2); ++i) B.v[i] = q[i];
 }
 
 // The same through 32-byte loads and stores, one whole DRAM sector a lane

@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(Cfg<BN, SWAP, QX, MX, PAIR, GROUPED>::kThreads
       const int64_t q0 = GROUPED ? row0_of(w) : (int64_t)tq * BN;
       float g_alpha = 0.0f;
       if constexpr (GROUPED) {
-        g_alpha = (float)(1.0 / ((double)__ldg(p.ga + w.g) * (double)__ldg(p.gw + w.g)));
+        g_alpha = (float)(1.0 / ((double)p.ga[w.g] * (double)p.gw[w.g]));
       }
       // A warp goes on as a whole or not at all.  Where the four warps share
       // staging buffers they also stop together, at the end of the first tile

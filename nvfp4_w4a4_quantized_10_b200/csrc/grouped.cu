@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const
   const int g_first = find_group(tab.off, p.E, (int)div_u32(c_begin, p.div_parts));
   const int g_last = find_group(tab.off, p.E, (int)div_u32(c_end - 1, p.div_parts));
   for (int i = threadIdx.x; i < (g_last - g_first + 1) * 8; i += 256)
-    quot[i >> 3][i & 7] = scale_quotient(__ldg(p.gs + g_first + (i >> 3)), i & 7);
+    quot[i >> 3][i & 7] = scale_quotient(p.gs[g_first + (i >> 3)], i & 7);
   __syncthreads();
   const uint32_t n = c_end - c_begin;
   const uint32_t begin = c_begin + n * warp / 8, end = c_begin + n * (warp + 1) / 8;
@@ -85,10 +85,10 @@ __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const
     const int j0 = (int)(item - row * p.parts) * p.seg * 32 + lane;
     const int j_end = min(p.nblk, j0 - lane + p.seg * 32);
     while ((int)row >= tab.off[g + 1]) ++g;
-    const float gs = __ldg(p.gs + g);
+    const float gs = p.gs[g];
     const float* q = quot[g - g_first];
     int64_t src = row;
-    if (p.row_index) src = __ldg(p.row_index + row);
+    if (p.row_index) src = p.row_index[row];
     const bool have = src >= 0 && src < p.M;
     if (!have && lane == 0) atomicCAS(p.err, 0u, kErrBounds);   // a row that x does not have: quantized as zeros
     const uint8_t* x = reinterpret_cast<const uint8_t*>(p.x) + (have ? src : 0) * src_bytes + (int64_t)j0 * kB;

@@ -31,12 +31,11 @@ struct GroupTable {
 // word is set and the table says that every group is empty, so no row is
 // touched.
 template <int kTileRows = 0>
-__device__ __forceinline__ void load_groups(GroupTable& t, const int32_t* __restrict__ offsets, int E, int64_t T,
-                                            unsigned* err) {
+__device__ __forceinline__ void load_groups(GroupTable& t, const int32_t* offsets, int E, int64_t T, unsigned* err) {
   bool bad = false;
   for (int i = threadIdx.x; i <= E; i += blockDim.x) {
-    const int o = __ldg(offsets + i);
-    const int next = i < E ? __ldg(offsets + i + 1) : o;
+    const int o = offsets[i];
+    const int next = i < E ? offsets[i + 1] : o;
     bad |= o < 0 || next < o || next > T || (i == 0 && o != 0);
     t.off[i] = o;
   }

@@ -4,6 +4,12 @@
 // %globaltimer; on expiry the waiting thread records NVFP4_ERR_TIMEOUT in the
 // device error word, raises the CTA's abort flag and returns false, so no
 // kernel of this library can spin forever.
+//
+// Kernels start as programmatic dependents, before the kernel ahead of them on
+// the stream has ended.  What that kernel may write is read by ordinary loads
+// (or TMA) behind griddepcontrol.wait, never through the read-only path
+// (ld.global.nc, __ldg), which is defined only for memory that nobody writes
+// while the reading kernel lives.
 #pragma once
 #include <cstdint>
 #include <cuda.h>

@@ -84,8 +84,8 @@ __device__ __forceinline__ float selected_value(uint32_t k) {
 
 template <bool kF32>
 __device__ __forceinline__ float load_logit(const void* p, int64_t i) {
-  if constexpr (kF32) return __ldg(reinterpret_cast<const float*>(p) + i);
-  else return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + i) << 16);
+  if constexpr (kF32) return reinterpret_cast<const float*>(p)[i];
+  else return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
 }
 
 // Experts in a row of the counts of all runs: rows start on 16 bytes.
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
   // the first pair of this thread is on its way while the counts are added up
   int id = -1, rank = 0;
   if (i < i_end) {
-    id = __ldg(p.ids + i);
+    id = p.ids[i];
     rank = p.slots[i];
   }
   const int quads = stride / 4, at = threadIdx.x % quads, rows = kRouteThreads / quads;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
   if ((int)threadIdx.x < rows * quads) {
 #pragma unroll 4
     for (int c = threadIdx.x / quads; c < (int)gridDim.x; c += rows) {
-      const int4 h = __ldg(reinterpret_cast<const int4*>(p.hist + (int64_t)c * stride) + at);
+      const int4 h = reinterpret_cast<const int4*>(p.hist + (int64_t)c * stride)[at];
       sum.x += h.x;
       sum.y += h.y;
       sum.z += h.z;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_slots_kernel(const RouteP
     if (i >= total) p.row_index[i] = -1;         // rows no pair fills
     i += kRouteThreads;
     if (i < i_end) {
-      id = __ldg(p.ids + i);
+      id = p.ids[i];
       rank = p.slots[i];
     }
   }
