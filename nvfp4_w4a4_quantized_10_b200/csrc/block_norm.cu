@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormP
         Block16<kF32> B[kCh][NB];
 #pragma unroll
         for (int c = 0; c < kCh; ++c) {
-          if (src[c] >= p.y_rows) {
+          if (src[c] >= p.y_rows || src[c] < -1) {
             atomicCAS(p.err, 0u, kErrBounds);                    // a row y does not have: skipped
             src[c] = -1;
           }
