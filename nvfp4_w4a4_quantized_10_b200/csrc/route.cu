@@ -66,20 +66,21 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ (k & 0x80000000u ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// bf16 logits: the key's upper half says all (the largest bf16 stands for
-// +inf), and the lower half holds the index, inverted, so that one maximum
-// finds value and lowest index together.
+// bf16 logits: the key's upper half says all (+inf keeps a key of its own,
+// above the largest bf16), and the lower half holds the index, inverted, so
+// that one maximum finds value and lowest index together.
 __device__ __forceinline__ uint32_t order_key_bf16(float x, int e) {
   if (!(x > -INFINITY)) return 0u;
-  const uint32_t b = __float_as_uint(fminf(__fadd_rn(x, 0.0f), __uint_as_float(0x7F7F0000u)));
+  const uint32_t b = __float_as_uint(__fadd_rn(x, 0.0f));
   return ((b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u)) & 0xFFFF0000u) | (0xFFFFu - (uint32_t)e);
 }
 
-// Value of a key: bf16 keys of negative numbers have their lower half set.
+// Value of a key: bf16 keys of negative numbers have their lower half set; the
+// key of +inf stands for the largest float, as in FP32.
 template <bool kF32>
 __device__ __forceinline__ float selected_value(uint32_t k) {
   if constexpr (kF32) return key_value(k);
-  else return key_value(k & 0x80000000u ? k & 0xFFFF0000u : k | 0xFFFFu);
+  else return fminf(key_value(k & 0x80000000u ? k & 0xFFFF0000u : k | 0xFFFFu), FLT_MAX);
 }
 
 template <bool kF32>
