@@ -477,7 +477,8 @@ NVFP4_API size_t nvfp4_grouped_scale_bytes(int64_t T, int n_groups, int64_t K);
  * encoding (bit for bit nvfp4_quantize's) with global scale global_scales[g] of
  *   act NONE    x[row_index[t]]         x device [M, K]
  *   act SWIGLU  silu(a) * b in FP32 for the row [a | b] = x[row_index[t]],
- *               x device [M, 2K]
+ *               x device [M, 2K]; a product beyond FP32 counts as the largest
+ *               float
  *   row_index     device int32[T], or NULL for row t itself (then M >= T).  An
  *                 index outside [0, M) sets the device error word
  *                 (NVFP4_ERR_DEVICE) and its row is quantized as zeros.

@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
+
 #include "block_quant.cuh"
 #include "common.h"
 #include "gemm_host.h"
@@ -121,6 +123,11 @@ __global__ void __launch_bounds__(256, kQuantCtas) grouped_quantize_kernel(const
           for (int i = 0; i < 16; ++i) {
             f[i] = silu(f[i]) * up[i];
             amax = fmaxf(amax, fabsf(f[i]));
+          }
+          if (amax > FLT_MAX) {                 // a product beyond FP32 counts as the largest float
+            amax = FLT_MAX;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = fminf(fmaxf(f[i], -FLT_MAX), FLT_MAX);
           }
         } else {
           amax = block_amax<kF32>(B[u]);
