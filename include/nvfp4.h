@@ -638,6 +638,19 @@ NVFP4_API nvfp4_status nvfp4_test_gemm_stalled_reduction(const uint8_t* a_codes,
                                                int64_t N, int64_t K, void* out, nvfp4_out_dtype out_dtype,
                                                int noalloc, nvfp4_stream_t stream);
 
+/* Test entry for the failure path of the block norm's staged rows: runs
+ * nvfp4_block_norm on y and residual (which may be NULL) into out, without
+ * norms, except that rows from stalled_from on are never copied into shared
+ * memory.  The bounded waits for them run out (set the bound with
+ * nvfp4_set_wait_timeout_ns), NVFP4_ERR_TIMEOUT is recorded and the kernel
+ * ends; rows from stalled_from on are not reliable, those before are right.
+ * Errors: as nvfp4_block_norm; INVALID_ARG for stalled_from outside [0, M],
+ * UNSUPPORTED for shapes whose rows are not staged (64 KB or longer, the
+ * inputs of a row in 222 KB, more than two rows an SM). */
+NVFP4_API nvfp4_status nvfp4_test_block_norm_stalled(const void* y, nvfp4_in_dtype dtype, int64_t M, int64_t K,
+                                           const void* residual, int64_t stalled_from, void* out,
+                                           nvfp4_stream_t stream);
+
 /* Measurement utility (no counterpart in the pages): the dense FP4
  * tensor-core throughput of the current device.  One CTA per SM issues
  * `iters` x 4 back-to-back tcgen05.mma kind::mxf4nvf4 block_scale

@@ -98,6 +98,7 @@ _lib.nvfp4_set_decode_cooperative.restype = None
 _lib.nvfp4_test_wait_timeout.argtypes = [ctypes.c_uint64, _vp]
 _lib.nvfp4_test_gemm_stalled_reduction.argtypes = [_vp, _vp, _f32, _vp, _vp, _f32, _i64, _i64, _i64, _vp,
                                                    ctypes.c_int, ctypes.c_int, _vp]
+_lib.nvfp4_test_block_norm_stalled.argtypes = [_vp, ctypes.c_int, _i64, _i64, _vp, _i64, _vp, _vp]
 _lib.nvfp4_measure_mma_peak.argtypes = [ctypes.c_int, ctypes.POINTER(ctypes.c_double),
                                         ctypes.POINTER(ctypes.c_double), _vp]
 _lib.nvfp4_status_string.restype = ctypes.c_char_p
@@ -480,6 +481,15 @@ def nvfp4_test_gemm_stalled_reduction(a_codes, a_scales, a_global_scale, w_codes
            _lib.nvfp4_test_gemm_stalled_reduction(_ptr(a_codes), _ptr(a_scales), float(a_global_scale),
                                                   _ptr(w_codes), _ptr(w_scales), float(w_global_scale), M, N, K,
                                                   _ptr(out), _out_dtype(out), int(bool(noalloc)), _stream(out)))
+
+
+def nvfp4_test_block_norm_stalled(y: torch.Tensor, stalled_from: int, out: torch.Tensor,
+                                  residual: torch.Tensor | None = None) -> None:
+    M, K = y.shape
+    d = _device_index(y)
+    _call("nvfp4_test_block_norm_stalled", _lib.nvfp4_test_block_norm_stalled, d, _at("y", y, y.dtype, None, d),
+          _in_dtype(y), M, K, _at("residual", residual, y.dtype, (M, K), d), int(stalled_from),
+          _at("out", out, y.dtype, (M, K), d))
 
 
 def nvfp4_measure_mma_peak(iters: int = 5000, device=None):

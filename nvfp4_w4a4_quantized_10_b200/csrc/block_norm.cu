@@ -51,6 +51,7 @@ struct NormParams {
   int64_t kc;
   uint64_t codes_bytes, scale_bytes, row_elems;
   int ring_slots;          // staged kernel
+  int64_t put_rows;        // rows that are copied into the ring: M (fewer in the failure-path test)
   uint64_t timeout_ns, drain_ns;
   int ahead;               // one block a thread: a CTA fetches the rows of the one so far on into L2
   int wide;                // every row and weight starts on a 32-byte boundary
@@ -153,7 +154,7 @@ __device__ __forceinline__ uint32_t ring_take(RowRing& r, const NormParams& p, v
 }
 
 __device__ __forceinline__ void ring_put(RowRing& r, const NormParams& p, volatile int* abort_flag) {
-  if (r.put_row >= p.M || *abort_flag) return;
+  if (r.put_row >= p.put_rows || *abort_flag) return;
   const void* src = r.put_array == 0 ? p.y : r.put_array == 1 && p.gate ? p.gate : p.residual;
   const uint32_t bar = r.bars + 8 * r.put_slot;
   mbar_arrive_expect_tx(bar, r.bytes);
@@ -496,6 +497,18 @@ cudaError_t launch_norm_staged(NormParams& p, const DeviceInfo* d, int threads, 
                       attr[0][d->device]);
 }
 
+// Staged: rows of at least 64 KB without slots whose inputs fit in the ring,
+// and more than two of them an SM.  In 4 bytes, 1003 x 17408, gate, residual
+// and two norms: 69.8 us, not staged 80.5 (150 rows: 21.0 and 20.1); 2048 x
+// 16384: 117 and 138; 2048 x 20480, residual and norm: 109 and 116; in 2
+// bytes, 1024 x 32768: 50.6 and 56.3, with gate and two norms 91.0 and 89.9.
+// On shorter rows the one CTA's instructions show: 2048 x 10240 in 4 bytes,
+// gate and two norms 93.2 and 86.1, 2048 x 17408 in 2 bytes 101 and 79.7.
+bool staged(const NormParams& p, bool f32, const DeviceInfo* d) {
+  const int64_t row = p.K * (f32 ? 4 : 2), inputs = (1 + (p.gate != nullptr) + (p.residual != nullptr)) * row;
+  return !p.slots && p.M > 2 * d->sm_count && row >= kRingRow && inputs <= kRingBytes;
+}
+
 // Rows of at most 1024 elements: a warp each, 8 to a CTA.  Longer ones: a CTA
 // each, with one 16-element block a thread while registers allow (K up to
 // 8192), then two (18432), then four.
@@ -513,15 +526,7 @@ cudaError_t launch_norm(NormParams& p, const DeviceInfo* d, cudaStream_t st) {
   auto threads = [&](int nb) { return (int)ceil_div(ceil_div(nblk, nb), 32) * 32; };
   if (nblk <= 320) return launch_norm_as<kF32, 1, false, 320, 4>(p, grid, threads(1), st);
   if (nblk <= 512) return launch_norm_as<kF32, 1, false, 512, 2>(p, grid, threads(1), st);
-  // Staged: rows of at least 64 KB without slots whose inputs fit in the ring,
-  // and more than two of them an SM.  In 4 bytes, 1003 x 17408, gate, residual
-  // and two norms: 69.8 us, not staged 80.5 (150 rows: 21.0 and 20.1); 2048 x
-  // 16384: 117 and 138; 2048 x 20480, residual and norm: 109 and 116; in 2
-  // bytes, 1024 x 32768: 50.6 and 56.3, with gate and two norms 91.0 and 89.9.
-  // On shorter rows the one CTA's instructions show: 2048 x 10240 in 4 bytes,
-  // gate and two norms 93.2 and 86.1, 2048 x 17408 in 2 bytes 101 and 79.7.
-  const int64_t row = p.K * (kF32 ? 4 : 2), inputs = (1 + (p.gate != nullptr) + (p.residual != nullptr)) * row;
-  if (!p.slots && p.M > 2 * d->sm_count && row >= kRingRow && inputs <= kRingBytes) {
+  if (staged(p, kF32, d)) {
     if constexpr (kF32)                            // (in 2 bytes only longer rows have 64 KB)
       if (nblk <= 2 * 576) return launch_norm_staged<kF32, 2, 576>(p, d, threads(2), st);
     return launch_norm_staged<kF32, 4, 512>(p, d, threads(4), st);
@@ -530,19 +535,13 @@ cudaError_t launch_norm(NormParams& p, const DeviceInfo* d, cudaStream_t st) {
   return launch_norm_as<kF32, 4, false, 512, 1>(p, grid, threads(4), st);
 }
 
-}  // namespace
-}  // namespace nvfp4
-
-using namespace nvfp4;
-
-extern "C" {
-
-nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, int64_t K, int64_t y_rows,
-                              const int32_t* slots, const float* slot_weights, int top_k, const float* post_weight,
-                              int64_t post_width, const void* gate, nvfp4_gate gate_kind, const void* residual,
-                              float residual_scale, void* residual_out, const float* pre_weight, float eps, void* out,
-                              uint8_t* codes, uint8_t* block_scales, float global_scale, nvfp4_sf_layout layout,
-                              nvfp4_stream_t stream) {
+// stalled_from: the failure-path test's first row that no copy brings, or -1.
+nvfp4_status run_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, int64_t K, int64_t y_rows,
+                            const int32_t* slots, const float* slot_weights, int top_k, const float* post_weight,
+                            int64_t post_width, const void* gate, nvfp4_gate gate_kind, const void* residual,
+                            float residual_scale, void* residual_out, const float* pre_weight, float eps, void* out,
+                            uint8_t* codes, uint8_t* block_scales, float global_scale, nvfp4_sf_layout layout,
+                            int64_t stalled_from, nvfp4_stream_t stream) {
   if (!y || M < 1 || K < 32 || K % 32 != 0) return NVFP4_ERR_INVALID_ARG;
   if (dtype != NVFP4_IN_BF16 && dtype != NVFP4_IN_F32) return NVFP4_ERR_INVALID_ARG;
   if ((slots == nullptr) != (slot_weights == nullptr)) return NVFP4_ERR_INVALID_ARG;
@@ -601,9 +600,37 @@ nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, in
   for (const void* q : {y, (const void*)post_weight, gate, residual, (const void*)residual_out,
                         (const void*)pre_weight, (const void*)out})
     if (reinterpret_cast<uintptr_t>(q) & 31) p.wide = 0;
+  p.put_rows = stalled_from < 0 ? M : stalled_from;
   p.err = d->err_word;
+  if (stalled_from >= 0 && !staged(p, dtype == NVFP4_IN_F32, d)) return NVFP4_ERR_UNSUPPORTED;
   cudaStream_t st = (cudaStream_t)stream;
   return cuda_status(dtype == NVFP4_IN_F32 ? launch_norm<true>(p, d, st) : launch_norm<false>(p, d, st));
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+nvfp4_status nvfp4_block_norm(const void* y, nvfp4_in_dtype dtype, int64_t M, int64_t K, int64_t y_rows,
+                              const int32_t* slots, const float* slot_weights, int top_k, const float* post_weight,
+                              int64_t post_width, const void* gate, nvfp4_gate gate_kind, const void* residual,
+                              float residual_scale, void* residual_out, const float* pre_weight, float eps, void* out,
+                              uint8_t* codes, uint8_t* block_scales, float global_scale, nvfp4_sf_layout layout,
+                              nvfp4_stream_t stream) {
+  return run_block_norm(y, dtype, M, K, y_rows, slots, slot_weights, top_k, post_weight, post_width, gate, gate_kind,
+                        residual, residual_scale, residual_out, pre_weight, eps, out, codes, block_scales, global_scale,
+                        layout, -1, stream);
+}
+
+nvfp4_status nvfp4_test_block_norm_stalled(const void* y, nvfp4_in_dtype dtype, int64_t M, int64_t K,
+                                           const void* residual, int64_t stalled_from, void* out,
+                                           nvfp4_stream_t stream) {
+  if (stalled_from < 0 || stalled_from > M) return NVFP4_ERR_INVALID_ARG;
+  return run_block_norm(y, dtype, M, K, M, nullptr, nullptr, 0, nullptr, 0, nullptr, NVFP4_GATE_NONE, residual, 1.0f,
+                        nullptr, nullptr, 1e-6f, out, nullptr, nullptr, 1.0f, NVFP4_SF_TCGEN05, stalled_from, stream);
 }
 
 }  // extern "C"
