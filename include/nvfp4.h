@@ -45,7 +45,8 @@
  *     returns its status and launches nothing.  Launch failures return
  *     NVFP4_ERR_CUDA.  Faults found by the kernels themselves (a bounded wait
  *     that ran out) are recorded in a per-device error word, read back by
- *     nvfp4_last_device_error().  No exception or abort crosses this ABI.
+ *     nvfp4_last_device_error(); what a call wrote whose wait ran out is not
+ *     reliable.  No exception or abort crosses this ABI.
  *   - Numbers in the format (readings of the pages, which name the formats
  *     but not their encodings): E2M1 = OCP FP4 (bit 3 sign, 2 exponent bits
  *     with bias 1, 1 mantissa bit: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6);
@@ -261,6 +262,8 @@ NVFP4_API nvfp4_status nvfp4_release_workspaces(void);
  * kernel writes declared memory while a library call that reads it may run;
  * writing it anyway (for example, quantizing new weights into it just before
  * a GEMM on the same stream) can make that GEMM read stale weights.
+ * nvfp4_grouped_gemm takes no notice of declarations: it reads its offsets,
+ * which the kernel before it may write, before any weight.
  * Declarations accumulate until nvfp4_forget_static().
  * Errors: INVALID_ARG (NULL base or zero bytes). */
 NVFP4_API nvfp4_status nvfp4_declare_static(const void* base, size_t bytes);
@@ -544,8 +547,9 @@ NVFP4_API nvfp4_status nvfp4_grouped_gemm(const uint8_t* a_codes, const uint8_t*
  *            codes, global_scale and layout are not looked at.
  * residual_out and out may each be the same buffer as residual or gate (or y
  * without slots), element for element; no other overlap is allowed, and not
- * with each other.  At least one output.  Inputs finite with squares whose row
- * sum stays below 3e38; eps finite and > 0; residual_scale finite.
+ * with each other.  At least one output.  Inputs finite; the squares of y, of b
+ * at each step and of v, summed over a row, below 3e38; h finite; eps finite
+ * and > 0; residual_scale finite.
  * K % 32 == 0, K <= 32768.  All pointers 16-byte aligned (slots and their
  * weights 4-byte).
  * Errors: INVALID_ARG, UNSUPPORTED (not sm_100, K beyond the limit),

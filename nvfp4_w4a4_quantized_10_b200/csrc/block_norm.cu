@@ -170,13 +170,19 @@ __device__ __forceinline__ void ring_put(RowRing& r, const NormParams& p, volati
 // NB: 16-element blocks of a thread; kWarpRow: a warp owns a row (K <= 512
 // NB), else a CTA does.  One row and done: the block scheduler then keeps
 // every SM's loads coming while other rows wait in their reductions (16384 x
-// 5120 bf16, residual and norm: 121 us; a persistent grid of 2, 3, 4 or 6 CTAs
-// an SM that walks the rows: 143, 168, 129, 148).
+// 5120 bf16, residual and norm, with 16-byte accesses: 121 us; a persistent
+// grid of 2, 3, 4 or 6 CTAs an SM that walks the rows: 143, 168, 129, 148; 98 us
+// with 32-byte accesses, one barrier a sum and the register caps below).
 // kStaged: that persistent grid for the longest rows, one CTA an SM, with rows
 // on their way by bulk copies while others are computed (RowRing).
 // kThreads, kCtas: the CTA's most threads, and CTAs that are to fit on an SM
 // (which caps the registers; 48 of them instead of 56 are 4 CTAs instead of 3
-// and 99 instead of 108 us in that case).
+// and 99 instead of 108 us in that case).  The caps were measured without
+// slots.  Two CTAs of 576 threads (NB = 2) have 56 registers, and spill 44 to
+// 112 bytes a thread in bf16 and 64 to 520 in FP32 (most with slots and gate);
+// of 512 threads (NB = 1) only with slots, 64 to 216.  Combines of 8 rows of
+// 9216 into 2048: 80 us in bf16 (79 % of the copy bandwidth), 162 in FP32 (78 %),
+// 187 with a gate (74 %).
 template <bool kF32, int NB, bool kWarpRow, bool kSlots, bool kGate, int kThreads, int kCtas, bool kStaged = false>
 __global__ void __launch_bounds__(kThreads, kCtas) block_norm_kernel(const NormParams p) {
   __shared__ float red_s[kStaged ? 4 : 2][32];

@@ -50,8 +50,9 @@ struct GroupedQuantParams {
 // Bound: HBM writes 9/16 byte an element and reads each source row once, but a
 // row gathered k times is read k - 1 times from L2 and encoded k times, and
 // the encoding (some 140 instructions a block) is what it waits for: 2048 rows
-// of 5120 gathered 8 times take 31 us, and took 42 with a flat loop over blocks
-// (214 instructions each); 16384 rows once, 37 us (5.8 TB/s).
+// of 5120 gathered 8 times take 31 us back to back (37 with cold caches; issue
+// slots 59 % busy), and took 42 with a flat loop over blocks (214 instructions
+// each); 16384 rows once, 37 us (5.8 TB/s).
 // Three CTAs an SM: all resident, with one prologue each (4 of them with fewer
 // registers took 33.1 us in the gathered case, 6 in two waves 37).
 constexpr int kQuantCtas = 3;

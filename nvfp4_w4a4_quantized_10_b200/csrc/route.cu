@@ -8,9 +8,11 @@
 //   slot(m, e) = offset_e + #{m' < m : m' selects e}
 //
 // The bytes (logits once, 16 a pair) take a microsecond at any size met in
-// serving; what both kernels wait for is instructions and latency (8 tokens
-// of 64 experts 3.4 us; 16384 of 128, top 8, 16.3 us, some 550 warp
-// instructions a token in the first kernel).
+// serving.  8 tokens of 64 experts take 3.4 us, all latency.  16384 of 128, top
+// 8, take 16.3 us: the first kernel's 550 warp instructions a token are 8 us of
+// the machine's issue slots, which are busy 68 % of its time (each round of the
+// selection waits for the one before); the second waits for ids and counts
+// (issue slots 26 % busy).
 //
 // Selection: one warp a token, each lane holding E / 32 logits as ordered
 // 32-bit keys; a round is one warp-wide integer maximum for the key and, for
@@ -118,9 +120,13 @@ __device__ __forceinline__ int warp_exclusive(int* v, int E) {
 
 // kOne: the grid is one cluster, each CTA has at most kSub tokens, and ranks
 // become slots here.  Else they are ranks inside the CTA's run.
-// Registers for one CTA an SM: with room for two, grids smaller than the
+// No second CTA an SM is asked for, and from 65 experts on (FP32: 33) the
+// registers leave room for one: with room for two, grids smaller than the
 // machine are doubled up on some SMs (8192 tokens of 128 experts 15.1 us
-// instead of 11.1; 16384, a run on every SM, 15.2 instead of 16.3).
+// instead of 11.1; 16384, a run on every SM, 15.2 instead of 16.3).  Instances
+// for fewer experts have 32 registers, so two fit (bf16 of 33 to 64 experts
+// spill 32 bytes): 16384 tokens of 32 experts in bf16 take 10.6 us, of 64 12.2,
+// 8192 of 32 10.4.
 template <bool kF32, int NV, bool kOne>
 __global__ void __launch_bounds__(kRouteThreads) route_topk_kernel(const RouteParams p) {
   __shared__ uint32_t mask[kMaxGroups][kSub / 32];
