@@ -62,7 +62,10 @@ cudaError_t get_workspace(const DeviceInfo* d, cudaStream_t st, int bn, Workspac
   w.owned = true;
   cudaError_t e = cudaMalloc(&w.ws, w.bytes);
   if (e != cudaSuccess) return e;
-  e = cudaMemset(w.ws, 0, w.bytes);
+  // on the call's own stream: the default stream's work is not ordered before a
+  // kernel on a non-blocking one, and words cleared under a running kernel are
+  // partials that its adders wait for
+  e = cudaMemsetAsync(w.ws, 0, w.bytes, st);
   if (e != cudaSuccess) {
     cudaFree(w.ws);
     return e;
