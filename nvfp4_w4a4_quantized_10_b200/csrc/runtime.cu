@@ -99,6 +99,9 @@ nvfp4_status nvfp4_last_device_error(void) {
   const unsigned zero = 0;
   if (cudaMemcpy(d->err_word, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
     return NVFP4_ERR_CUDA;
+  // (a copy from pageable memory may return before it lands, and would then
+  // wipe what a later kernel on a non-blocking stream reports)
+  if (cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (w != 0 && clear_gemm_scratch(d->device) != cudaSuccess) return NVFP4_ERR_CUDA;
   if (w == kErrTimeout) return NVFP4_ERR_TIMEOUT;
   if (w != 0) return NVFP4_ERR_DEVICE;
